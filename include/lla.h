@@ -339,6 +339,134 @@ int hla_decode_attn(const hla_decode_params *p, void *ws, size_t ws_bytes,
 #define LLA_NOALLOC_SCRATCH_BYTES (32u * 1024u * 1024u)
 int hla_decode_attn_noalloc(const hla_decode_params *p, lla_stream stream);
 
+/* ------------------------------------------------------------------------ */
+/* (d) 8-bit K/V cache: writer, attention, eviction                          */
+/* ------------------------------------------------------------------------ */
+/* A cache of exact K/V vectors of one loop and layer, or of per-head latents
+ * (LLA abstract, per-head codec), held in 8 bits: for each head one code per
+ * element, and one fp32 scale per part (K, V) for each block of `block`
+ * tokens.  The stored value of an element is code * scale.  The HLA summary
+ * names quantisation and token eviction as what latent caches combine with
+ * ("Conclusion / Future directions"); the format is this library's:
+ *   s = amax / top over the block's tokens and the head's d elements (top =
+ *   127 for int8 codes, 448 for e4m3), code = x / s rounded to nearest-even;
+ *   both quotients in fp32.  A block of zeros has s = 0 and zero codes; a block
+ *   that holds an infinity or a NaN has s = NaN and zero codes, and every read
+ *   of it gives NaN.
+ * Rows of a cache past a sequence's length may hold anything; no call reads
+ * them into a result.  A sequence's last block may be partly filled. */
+typedef enum { LLA_KV8_E4M3 = 0, LLA_KV8_I8 = 1 } lla_kv8_code;
+
+typedef struct {
+  int32_t B, H, d;         /* sequences, cache heads, head dim: a multiple of
+                              16 up to 256                                      */
+  int32_t block, Ncap;     /* tokens per scale (16, 32, 64, 128 or 256); rows
+                              per sequence, a multiple of block                 */
+  int32_t code;            /* lla_kv8_code                                      */
+  void *k, *v;             /* codes [B, H, Ncap, d], rows dense                 */
+  int64_t stride_b, stride_h;             /* multiples of 16; of a cache that a
+                              call only reads, sequences or heads may share rows
+                              (stride 0); rows that are written are apart       */
+  float *k_scale, *v_scale;               /* [B, H, Ncap / block], inner dense  */
+  int64_t scale_stride_b, scale_stride_h;
+} lla_kv8_cache;
+
+/* Per-sequence values.  `at` NULL: `all` holds for every sequence; else a
+ * device array of B values, read when the kernels run (so a captured graph
+ * follows it).  Values outside their range are clamped to it unless a field
+ * says otherwise; no value leads to an access outside the caller's buffers. */
+typedef struct { const int32_t *at; int32_t all; } lla_i32;
+
+typedef struct {
+  lla_kv8_cache cache;
+  /* Source: [B, rows, H, d], LLA_F32 or LLA_BF16, d dense, 16-byte aligned.
+   * ring = 0: token p of the call is row src0 + p (src0 + n <= rows).
+   * ring = 1: it is row (src0 + p) mod rows, the exact window's slot of
+   * position src0 + p (n <= rows). */
+  const void *x_k, *x_v;
+  int32_t dtype, rows, ring;
+  int64_t x_stride_b, x_stride_n, x_stride_h;
+  int32_t max_n;           /* no sequence writes more tokens than this          */
+  lla_i32 n, src0, row0;   /* tokens written; first source row or position;
+                              first cache row.  Rows [row0, row0 + n) and the
+                              scales of their blocks are overwritten.  A
+                              sequence whose row0 is no multiple of block, or
+                              whose rows do not fit the cache (ring = 0: the
+                              source), is left as it was.                       */
+} lla_kv8_write_params;
+
+/* Quantise n tokens of each sequence into whole blocks of the cache: the
+ * blocks that start in [row0, row0 + n), the last of them up to row0 + n only
+ * (its scale covers the tokens written).  To fill such a block up, write it
+ * again from its first token.  No workspace. */
+int lla_kv8_write(const lla_kv8_write_params *p, lla_stream stream);
+
+typedef struct {
+  lla_kv8_cache cache;
+  lla_i32 len;             /* cached tokens, 0..Ncap: all seen by every query   */
+  int32_t nq, G;           /* query positions (the last nq of the context) and
+                              query heads per cache head (grouped heads, or the
+                              loops that share a per-head latent)               */
+  const void *q;           /* [B, nq, H * G, d]: head h reads cache head h / G;
+                              post-rotary, or absorbed; inner [H * G, d] dense  */
+  void *out;               /* as q, LLA_F32 or LLA_BF16; may not overlap inputs */
+  int32_t dtype;           /* of q and out                                      */
+  int64_t q_stride_b, q_stride_n, out_stride_b, out_stride_n;
+  /* Exact tokens after the cached ones: the last `tail` positions of a context
+   * of ctx tokens, position j in ring slot j mod Wcap.  Query position p of the
+   * call is context position ctx - nq + p and sees those up to its own.
+   * win_k NULL: none (ctx and tail are not read). */
+  const void *win_k, *win_v;              /* [B, Wcap, H, d], d dense           */
+  int32_t win_dtype, Wcap;
+  int64_t win_stride_b, win_stride_n, win_stride_h;
+  lla_i32 ctx, tail;       /* tail 0..Wcap                                      */
+  float scale;             /* 0 -> 1/sqrt(d)                                    */
+  /* Optional accumulator [B, H, Ncap] fp32 (NULL: none): the softmax weight of
+   * each cached token, summed over the call's nq * G queries of its head, is
+   * added; entries from len on are left as they are.  Deterministic: no
+   * atomics. */
+  float *weights;
+  int64_t weights_stride_b, weights_stride_h;
+} lla_kv8_attn_params;
+
+/* o = sum_j a_j v_j, a = softmax(scale * q . k_j) over the cached tokens and
+ * the visible exact ones jointly.  A query that sees no token gives zeros.
+ * Precision: codes are exact in the products; queries and probabilities enter
+ * them as one f16 term for bf16 output, as two (about 22 bits) for fp32;
+ * statistics and sums are fp32. */
+size_t lla_kv8_attn_workspace_bytes(const lla_kv8_attn_params *p);
+int lla_kv8_attn(const lla_kv8_attn_params *p, void *ws, size_t ws_bytes, lla_stream stream);
+
+typedef struct {
+  lla_kv8_cache src, dst;  /* same B, H, d, block, code; dst either is src (same
+                              pointers and strides: in place) or overlaps
+                              neither it nor its weights                        */
+  const float *weights;    /* [B, H, src.Ncap], as lla_kv8_attn adds them up    */
+  int64_t weights_stride_b, weights_stride_h;
+  float *dst_weights;      /* [B, H, dst.Ncap]; `weights` itself in place       */
+  int64_t dst_weights_stride_b, dst_weights_stride_h;
+  const int32_t *len;      /* device [B]: tokens of each sequence, 0..src.Ncap  */
+  int32_t *dst_len;        /* device [B], written; may be `len` itself          */
+  int32_t keep;            /* blocks kept per head, <= src.Ncap / block and
+                              <= dst.Ncap / block                               */
+  int32_t first, last;     /* of these, the first and the last blocks that are
+                              always kept; last >= 1, first + last <= keep      */
+  int32_t *kept;           /* optional [B, H, keep] dense: the source block of
+                              each kept block, -1 where there is none           */
+} lla_kv8_evict_params;
+
+/* Keep the `keep` blocks of each head that gathered the most weight.  A
+ * sequence of at most keep blocks is kept whole.  Of a longer one, the first
+ * `first` and the last `last` blocks are kept and, of those between, the ones
+ * whose tokens' weights sum highest (fp64 sum rounded to fp32; NaN ranks last;
+ * of equal sums the lower block wins).  Kept blocks stay in order and move to
+ * the front with their scales and weights; each head keeps its own.  Its new
+ * length, dst_len, is the old one less the evicted blocks' tokens.  Rows of dst
+ * past it are left as they are, dst_weights from dst_len to the old length (as
+ * far as dst reaches) is set to zero. */
+size_t lla_kv8_evict_workspace_bytes(const lla_kv8_evict_params *p);
+int lla_kv8_evict(const lla_kv8_evict_params *p, void *ws, size_t ws_bytes, lla_stream stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -12,19 +12,24 @@ Entry points (names as in the C ABI):
   encoders; appends rows to a caller-owned latent cache.
 * ``lla_decode_attn``    -- LLA reconstruct-on-read decode attention.
 * ``hla_decode_attn``    -- absorbed latent read: HLA (eqs. 3-4) and LLA-D.
+* ``lla_kv8_write``, ``lla_kv8_attn``, ``lla_kv8_evict`` -- an 8-bit K/V cache
+  with a scale for each block of tokens and head: its writer, the attention
+  that reads it beside the exact window, eviction by accumulated weight.
 """
 
 import ctypes
 
 from . import _abi
-from ._abi import (LLA_BF16, LLA_ERR_CUDA, LLA_F32, LLA_FP8_E4M3, LLA_WRITE_FOLDED, LLA_WRITE_HLA,  # noqa: F401
-                   LLA_WRITE_PERHEAD, LibraryMissing)
+from ._abi import (LLA_BF16, LLA_ERR_CUDA, LLA_F32, LLA_FP8_E4M3, LLA_KV8_E4M3, LLA_KV8_I8,  # noqa: F401
+                   LLA_WRITE_FOLDED, LLA_WRITE_HLA, LLA_WRITE_PERHEAD, LibraryMissing)
 
 __all__ = [
     "LLAError", "lla_status_str", "lla_abi_version",
     "lla_write_latents", "lla_write_workspace_bytes",
     "lla_decode_attn", "lla_decode_workspace_bytes",
     "hla_decode_attn", "hla_decode_workspace_bytes",
+    "lla_kv8_write", "lla_kv8_attn", "lla_kv8_attn_workspace_bytes",
+    "lla_kv8_evict", "lla_kv8_evict_workspace_bytes",
     "LLA_WRITE_HLA", "LLA_WRITE_PERHEAD", "LLA_WRITE_FOLDED",
 ]
 
@@ -401,3 +406,208 @@ def lla_decode_attn(*, workspace=None, stream=None, **kw):
     need = L.lla_decode_workspace_bytes(ctypes.byref(p))
     ws, nb = _workspace(need, dev, workspace)
     _call(L.lla_decode_attn, p, ws, nb, _stream_handle(stream, dev), "lla_decode_attn")
+
+
+# -------------------------------------------------------- 8-bit K/V cache --
+def _kv8_cache(k8, v8, k_scale, v_scale):
+    """[B,H,Ncap,d] codes and [B,H,Ncap/block] scales as the ABI's struct."""
+    torch = _torch()
+    if k8.dtype == torch.int8:
+        code = LLA_KV8_I8
+    elif k8.dtype == torch.float8_e4m3fn:
+        code = LLA_KV8_E4M3
+    else:
+        raise TypeError(f"unsupported code dtype {k8.dtype}; use int8 or float8_e4m3fn")
+    if v8.dtype != k8.dtype or k_scale.dtype != torch.float32 or v_scale.dtype != torch.float32:
+        raise TypeError("k8 and v8 share a dtype, scales are float32")
+    shape, sshape = k8.shape, k_scale.shape
+    if len(shape) != 4 or v8.shape != shape or v8.stride() != k8.stride():
+        raise ValueError("k8 and v8 are [B,H,Ncap,d] with the same strides")
+    B, H, cap, d = shape
+    if (len(sshape) != 3 or v_scale.shape != sshape or v_scale.stride() != k_scale.stride() or sshape[0] != B
+            or sshape[1] != H or (cap % sshape[2] if sshape[2] else cap)):
+        raise ValueError("k_scale and v_scale are [B,H,Ncap/block] with the same strides")
+    _dense_inner(k8, 2, "k8")
+    _dense_inner(k_scale, 1, "k_scale")
+    st, ss = k8.stride(), k_scale.stride()
+    # an axis of one element may carry any stride
+    sh, ssh = (st[1] if H > 1 else cap * d), (ss[1] if H > 1 else sshape[2])
+    return _abi.Kv8Cache(B, H, d, cap // sshape[2] if sshape[2] else 16, cap, code, k8.data_ptr(), v8.data_ptr(),
+                         st[0] if B > 1 else H * sh, sh, k_scale.data_ptr(), v_scale.data_ptr(),
+                         ss[0] if B > 1 else H * ssh, ssh)
+
+
+def _i32(v, B, name):
+    """An int for every sequence, or an int32 tensor [B]."""
+    if isinstance(v, _torch().Tensor):
+        if v.dtype != _torch().int32 or v.dim() != 1 or v.shape[0] != B or not v.is_contiguous():
+            raise ValueError(f"{name} is an int or a contiguous int32 tensor [B]")
+        return _abi.I32(v.data_ptr(), 0)
+    return _abi.I32(None, int(v))
+
+
+def _tensors(*ts):
+    return [t for t in ts if isinstance(t, _torch().Tensor)]
+
+
+def _rows16(t, what):
+    """Strides of the outer axes, those of one element replaced by 0."""
+    _dense_inner(t, 1, what)
+    return [s if n > 1 else 0 for n, s in zip(t.shape[:-1], t.stride()[:-1])]
+
+
+def _on(dev, fn, where, params, *mid, stream):
+    """Call fn on dev's stream, with dev current."""
+    torch = _torch()
+    handle = _stream_handle(stream, dev)
+    if dev.index == torch.cuda.current_device():
+        st = fn(ctypes.byref(params), *mid, handle)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(ctypes.byref(params), *mid, handle)
+    if st != 0:
+        raise LLAError(st, where)
+
+
+def _kv8_workspace(nbytes, dev, workspace, stream):
+    if nbytes and workspace is None:
+        ws = _torch().empty(nbytes, dtype=_torch().uint8, device=dev)
+        if stream is not None:
+            ws.record_stream(stream)     # its memory is not handed out again before the call has run
+        return ws.data_ptr(), nbytes, ws
+    ptr, nb = _workspace(nbytes, dev, workspace)
+    return ptr, nb, workspace
+
+
+def lla_kv8_write(*, k, v, k8, v8, k_scale, v_scale, n=None, max_n=None, src0=0, row0=0, ring=False, stream=None):
+    """Quantise tokens of k, v [B,rows,H,d] (float32 or bfloat16) into the cache.
+
+    Cache: codes k8, v8 [B,H,Ncap,d] (int8 or float8_e4m3fn) and scales
+    k_scale, v_scale [B,H,Ncap/block] float32, block in 16..256.  Sequence b's
+    tokens src0[b] .. src0[b]+n[b]-1 (ring=True: positions, in rows mod `rows`)
+    go to cache rows row0[b].., row0 a multiple of block.  n, src0, row0: an int
+    for all sequences or an int32 CUDA tensor [B]; n defaults to `rows`, and a
+    tensor n needs max_n, its bound (default: the least of rows and Ncap).
+    """
+    dev = _cuda(k, v, k8, v8, k_scale, v_scale, *_tensors(n, src0, row0))
+    c = _kv8_cache(k8, v8, k_scale, v_scale)
+    if k.dim() != 4 or k.shape != v.shape or k.stride() != v.stride() or k.dtype != v.dtype:
+        raise ValueError("k and v are [B,rows,H,d] and match in shape, strides and dtype")
+    if k.shape[0] != c.B or k.shape[2] != c.H or k.shape[3] != c.d:
+        raise ValueError("k and v are [B,rows,H,d] of the cache's B, H and d")
+    rows = k.shape[1]
+    n = rows if n is None else n
+    if max_n is None:
+        max_n = n if isinstance(n, int) else min(rows, c.Ncap)
+    sb, sn, sh = _rows16(k, "k")
+    p = _abi.Kv8WriteParams(c, k.data_ptr(), v.data_ptr(), _dtype_code(k), rows, int(bool(ring)), sb, sn, sh,
+                            int(max_n), _i32(n, c.B, "n"), _i32(src0, c.B, "src0"), _i32(row0, c.B, "row0"))
+    _on(dev, lib().lla_kv8_write, "lla_kv8_write", p, stream=stream)
+
+
+def _kv8_attn_params(q, k8, v8, k_scale, v_scale, lens, out, win_k=None, win_v=None, ctx=None, tail=0, scale=0.0,
+                     weights=None):
+    c = _kv8_cache(k8, v8, k_scale, v_scale)
+    if q.dim() != 4 or q.shape[0] != c.B or q.shape[3] != c.d or q.shape[2] % c.H or q.shape[2] == 0:
+        raise ValueError("q is [B,nq,H*G,d] of the cache's B, H and d")
+    if out.shape != q.shape or out.dtype != q.dtype:
+        raise ValueError("out must have q's shape and dtype")
+    nq = q.shape[1]
+    _dense_inner(q, 2, "q")
+    _dense_inner(out, 2, "out")
+    qs, os_ = q.stride(), out.stride()
+    row = q.shape[2] * c.d
+    p = _abi.Kv8AttnParams(c, _i32(lens, c.B, "lens"), nq, q.shape[2] // c.H, q.data_ptr(), out.data_ptr(),
+                           _dtype_code(q), qs[0] if c.B > 1 else 0, qs[1] if nq > 1 else 0,
+                           os_[0] if c.B > 1 else nq * row, os_[1] if nq > 1 else row)
+    if win_k is not None:
+        if (win_v is None or win_k.dim() != 4 or win_k.shape != win_v.shape or win_k.stride() != win_v.stride()
+                or win_k.dtype != win_v.dtype):
+            raise ValueError("win_k and win_v are [B,Wcap,H,d] and match in shape, strides and dtype")
+        if win_k.shape[0] != c.B or win_k.shape[2] != c.H or win_k.shape[3] != c.d:
+            raise ValueError("win_k and win_v are [B,Wcap,H,d] of the cache's B, H and d")
+        if ctx is None:
+            raise ValueError("win_k needs ctx, the context length")
+        p.win_k, p.win_v, p.win_dtype, p.Wcap = win_k.data_ptr(), win_v.data_ptr(), _dtype_code(win_k), win_k.shape[1]
+        p.win_stride_b, p.win_stride_n, p.win_stride_h = _rows16(win_k, "win_k")
+        p.ctx, p.tail = _i32(ctx, c.B, "ctx"), _i32(tail, c.B, "tail")
+    elif win_v is not None:
+        raise ValueError("win_v without win_k")
+    p.scale = scale
+    if weights is not None:
+        p.weights, p.weights_stride_b, p.weights_stride_h = _kv8_weights(weights, c)
+    return p
+
+
+def _kv8_weights(w, c):
+    if w.dtype != _torch().float32 or tuple(w.shape) != (c.B, c.H, c.Ncap):
+        raise ValueError("weights are float32 [B,H,Ncap]")
+    _dense_inner(w, 1, "weights")
+    sh = w.stride(1) if c.H > 1 else c.Ncap
+    return w.data_ptr(), w.stride(0) if c.B > 1 else c.H * sh, sh
+
+
+def lla_kv8_attn_workspace_bytes(**kw):
+    kw.pop("workspace", None)
+    kw.pop("stream", None)
+    return lib().lla_kv8_attn_workspace_bytes(ctypes.byref(_kv8_attn_params(**kw)))
+
+
+def lla_kv8_attn(*, q, k8, v8, k_scale, v_scale, lens, out, win_k=None, win_v=None, ctx=None, tail=0, scale=0.0,
+                 weights=None, workspace=None, stream=None):
+    """Attention over an 8-bit cache and the exact tokens after it, one softmax.
+
+    q [B,nq,H*G,d] (float32 or bfloat16; head h reads cache head h // G), out
+    likewise; cache as lla_kv8_write fills it, of which each query sees the
+    first lens[b] tokens; ring win_k, win_v [B,Wcap,H,d] holds the last tail[b]
+    positions of a context of ctx[b] tokens, position j in row j mod Wcap, and
+    query p (context position ctx - nq + p) sees those up to its own.  lens,
+    ctx, tail: an int for all sequences or an int32 CUDA tensor [B].  weights
+    [B,H,Ncap] float32, optional: the softmax weights of the cached tokens are
+    added, summed over the queries of their head.  scale 0: 1/sqrt(d).
+    """
+    dev = _cuda(q, k8, v8, k_scale, v_scale, out, win_k, win_v, weights, *_tensors(lens, ctx, tail))
+    p = _kv8_attn_params(q, k8, v8, k_scale, v_scale, lens, out, win_k, win_v, ctx, tail, scale, weights)
+    L = lib()
+    ws, nb, _keep = _kv8_workspace(L.lla_kv8_attn_workspace_bytes(ctypes.byref(p)), dev, workspace, stream)
+    _on(dev, L.lla_kv8_attn, "lla_kv8_attn", p, ws, nb, stream=stream)
+
+
+def _kv8_evict_params(k8, v8, k_scale, v_scale, weights, lens, keep, first=0, last=1, to=None, kept=None):
+    c = _kv8_cache(k8, v8, k_scale, v_scale)
+    if to is None:
+        to = dict(k8=k8, v8=v8, k_scale=k_scale, v_scale=v_scale, weights=weights, lens=lens)
+    t = _kv8_cache(to["k8"], to["v8"], to["k_scale"], to["v_scale"])
+    for x, nm in ((lens, "lens"), (to["lens"], "to['lens']")):
+        if x.dtype != _torch().int32 or tuple(x.shape) != (c.B,) or not x.is_contiguous():
+            raise ValueError(f"{nm} is a contiguous int32 tensor [B]")
+    if kept is not None and (kept.dtype != _torch().int32 or tuple(kept.shape) != (c.B, c.H, keep)
+                             or not kept.is_contiguous()):
+        raise ValueError("kept is a contiguous int32 tensor [B,H,keep]")
+    return _abi.Kv8EvictParams(c, t, *_kv8_weights(weights, c), *_kv8_weights(to["weights"], t), lens.data_ptr(),
+                               to["lens"].data_ptr(), keep, first, last, None if kept is None else kept.data_ptr())
+
+
+def lla_kv8_evict_workspace_bytes(**kw):
+    kw.pop("workspace", None)
+    kw.pop("stream", None)
+    return lib().lla_kv8_evict_workspace_bytes(ctypes.byref(_kv8_evict_params(**kw)))
+
+
+def lla_kv8_evict(*, k8, v8, k_scale, v_scale, weights, lens, keep, first=0, last=1, to=None, kept=None,
+                  workspace=None, stream=None):
+    """Keep the `keep` blocks of each head that gathered the most weight.
+
+    Cache and weights [B,H,Ncap] as lla_kv8_attn reads and adds them; lens int32
+    [B].  Of a sequence of more than `keep` blocks the first `first`, the last
+    `last` (>= 1) and, of the others, those whose tokens' weights sum highest
+    stay, in order, moved to the front.  In place, or into `to`: a dict of k8,
+    v8, k_scale, v_scale, weights and lens of another cache (which may have
+    another Ncap).  kept [B,H,keep] int32, optional: source block of each block
+    that stays, -1 where there is none.
+    """
+    dev = _cuda(k8, v8, k_scale, v_scale, weights, lens, kept, *(to or {}).values())
+    p = _kv8_evict_params(k8, v8, k_scale, v_scale, weights, lens, keep, first, last, to, kept)
+    L = lib()
+    ws, nb, _keep = _kv8_workspace(L.lla_kv8_evict_workspace_bytes(ctypes.byref(p)), dev, workspace, stream)
+    _on(dev, L.lla_kv8_evict, "lla_kv8_evict", p, ws, nb, stream=stream)

@@ -27,6 +27,9 @@ LLA_WRITE_HLA = 0
 LLA_WRITE_PERHEAD = 1
 LLA_WRITE_FOLDED = 2
 
+LLA_KV8_E4M3 = 0
+LLA_KV8_I8 = 1
+
 c_i32 = ctypes.c_int32
 c_i64 = ctypes.c_int64
 c_f32 = ctypes.c_float
@@ -98,6 +101,62 @@ class HlaDecodeParams(ctypes.Structure):
     ]
 
 
+class I32(ctypes.Structure):
+    _fields_ = [("at", c_vp), ("all", c_i32)]
+
+
+class Kv8Cache(ctypes.Structure):
+    _fields_ = [
+        ("B", c_i32), ("H", c_i32), ("d", c_i32), ("block", c_i32), ("Ncap", c_i32), ("code", c_i32),
+        ("k", c_vp), ("v", c_vp),
+        ("stride_b", c_i64), ("stride_h", c_i64),
+        ("k_scale", c_vp), ("v_scale", c_vp),
+        ("scale_stride_b", c_i64), ("scale_stride_h", c_i64),
+    ]
+
+
+class Kv8WriteParams(ctypes.Structure):
+    _fields_ = [
+        ("cache", Kv8Cache),
+        ("x_k", c_vp), ("x_v", c_vp),
+        ("dtype", c_i32), ("rows", c_i32), ("ring", c_i32),
+        ("x_stride_b", c_i64), ("x_stride_n", c_i64), ("x_stride_h", c_i64),
+        ("max_n", c_i32),
+        ("n", I32), ("src0", I32), ("row0", I32),
+    ]
+
+
+class Kv8AttnParams(ctypes.Structure):
+    _fields_ = [
+        ("cache", Kv8Cache),
+        ("len", I32),
+        ("nq", c_i32), ("G", c_i32),
+        ("q", c_vp), ("out", c_vp),
+        ("dtype", c_i32),
+        ("q_stride_b", c_i64), ("q_stride_n", c_i64), ("out_stride_b", c_i64), ("out_stride_n", c_i64),
+        ("win_k", c_vp), ("win_v", c_vp),
+        ("win_dtype", c_i32), ("Wcap", c_i32),
+        ("win_stride_b", c_i64), ("win_stride_n", c_i64), ("win_stride_h", c_i64),
+        ("ctx", I32), ("tail", I32),
+        ("scale", c_f32),
+        ("weights", c_vp),
+        ("weights_stride_b", c_i64), ("weights_stride_h", c_i64),
+    ]
+
+
+class Kv8EvictParams(ctypes.Structure):
+    _fields_ = [
+        ("src", Kv8Cache), ("dst", Kv8Cache),
+        ("weights", c_vp),
+        ("weights_stride_b", c_i64), ("weights_stride_h", c_i64),
+        ("dst_weights", c_vp),
+        ("dst_weights_stride_b", c_i64), ("dst_weights_stride_h", c_i64),
+        ("len", c_vp), ("dst_len", c_vp),
+        ("keep", c_i32), ("first", c_i32), ("last", c_i32),
+        ("kept", c_vp),
+    ]
+
+
 # Every symbol include/lla.h declares, with its ctypes prototype.
 PROTOTYPES = {
     "lla_abi_version": (ctypes.c_int, []),
@@ -111,6 +170,11 @@ PROTOTYPES = {
     "hla_decode_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(HlaDecodeParams)]),
     "hla_decode_attn": (ctypes.c_int, [ctypes.POINTER(HlaDecodeParams), c_vp, ctypes.c_size_t, c_vp]),
     "hla_decode_attn_noalloc": (ctypes.c_int, [ctypes.POINTER(HlaDecodeParams), c_vp]),
+    "lla_kv8_write": (ctypes.c_int, [ctypes.POINTER(Kv8WriteParams), c_vp]),
+    "lla_kv8_attn_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(Kv8AttnParams)]),
+    "lla_kv8_attn": (ctypes.c_int, [ctypes.POINTER(Kv8AttnParams), c_vp, ctypes.c_size_t, c_vp]),
+    "lla_kv8_evict_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(Kv8EvictParams)]),
+    "lla_kv8_evict": (ctypes.c_int, [ctypes.POINTER(Kv8EvictParams), c_vp, ctypes.c_size_t, c_vp]),
 }
 
 # Size of the library's static scratch used by hla_decode_attn_noalloc.

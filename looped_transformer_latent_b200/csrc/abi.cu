@@ -309,6 +309,156 @@ HlaPlan plan_lla(const lla_decode_params& p) {
   return pl;
 }
 
+// -------------------------------------------------------- 8-bit K/V cache --
+// Whether n0 x n1 pieces of `extent` elements at strides s0, s1 are apart: a
+// condition for every plane that a call writes.
+bool apart(int64_t n0, int64_t s0, int64_t n1, int64_t s1, int64_t extent) {
+  if (n0 > 1 && s0 < extent) return false;
+  if (n1 > 1 && s1 < extent) return false;
+  return n0 <= 1 || n1 <= 1 || s0 >= (n1 - 1) * s1 + extent || s1 >= (n0 - 1) * s0 + extent;
+}
+
+bool cache_apart(const lla_kv8_cache& c) {
+  return apart(c.B, c.stride_b, c.H, c.stride_h, (int64_t)c.Ncap * c.d) &&
+         apart(c.B, c.scale_stride_b, c.H, c.scale_stride_h, c.Ncap / c.block);
+}
+
+// Sizes and layout of a cache; pointers only where it has anything in it.
+int check_cache(const lla_kv8_cache& c) {
+  if (c.B < 0 || c.H < 1 || c.Ncap < 0) return LLA_ERR_SHAPE;
+  if (c.code != LLA_KV8_E4M3 && c.code != LLA_KV8_I8) return LLA_ERR_DTYPE;
+  if (c.d < 16 || c.d > 256 || c.d % 16) return LLA_ERR_UNSUPPORTED;
+  if (c.block != 16 && c.block != 32 && c.block != 64 && c.block != 128 && c.block != 256) return LLA_ERR_UNSUPPORTED;
+  if (c.Ncap % c.block) return LLA_ERR_SHAPE;
+  if (c.B > 32767 || c.H > 65535) return LLA_ERR_UNSUPPORTED;   // grid axes (the writer's holds 2 B)
+  if (c.B == 0 || c.Ncap == 0) return LLA_OK;
+  if (!c.k || !c.v || !c.k_scale || !c.v_scale) return LLA_ERR_NULL;
+  if (!aligned(c.k, 16) || !aligned(c.v, 16) || c.stride_b % 16 || c.stride_h % 16) return LLA_ERR_ALIGN;
+  if (!aligned(c.k_scale, 4) || !aligned(c.v_scale, 4)) return LLA_ERR_ALIGN;
+  // sequences or heads that only read may share rows (stride 0)
+  if (c.stride_b < 0 || c.stride_h < 0 || c.scale_stride_b < 0 || c.scale_stride_h < 0) return LLA_ERR_SHAPE;
+  return LLA_OK;
+}
+
+int check_i32(const lla_i32& v) { return !v.at || aligned(v.at, 4) ? LLA_OK : LLA_ERR_ALIGN; }
+
+// A strided [.., d] tensor of 16-byte aligned rows.
+int check_rows(const void* x, int dtype, int64_t s0, int64_t s1, int64_t s2) {
+  const int64_t es = (int64_t)elem_size(dtype);
+  if (!aligned(x, 16) || s0 * es % 16 || s1 * es % 16 || s2 * es % 16) return LLA_ERR_ALIGN;
+  if (s0 < 0 || s1 < 0 || s2 < 0) return LLA_ERR_SHAPE;
+  return LLA_OK;
+}
+
+int check_kv8_write(const lla_kv8_write_params& p) {
+  int st = check_cache(p.cache);
+  if (st != LLA_OK) return st;
+  if (!dtype_ok(p.dtype)) return LLA_ERR_DTYPE;
+  if (p.rows < 0 || p.max_n < 0 || p.max_n > p.cache.Ncap || p.max_n > p.rows) return LLA_ERR_SHAPE;
+  for (const lla_i32* v : {&p.n, &p.src0, &p.row0})
+    if ((st = check_i32(*v)) != LLA_OK) return st;
+  if (!p.n.at && (p.n.all < 0 || p.n.all > p.max_n)) return LLA_ERR_SHAPE;
+  if (!p.row0.at && (p.row0.all < 0 || p.row0.all % p.cache.block)) return LLA_ERR_SHAPE;
+  if (!p.row0.at && !p.n.at && (int64_t)p.row0.all + p.n.all > p.cache.Ncap) return LLA_ERR_SHAPE;
+  if (!p.ring && !p.src0.at && (p.src0.all < 0 || (!p.n.at && (int64_t)p.src0.all + p.n.all > p.rows)))
+    return LLA_ERR_SHAPE;
+  if (p.cache.B == 0 || p.max_n == 0) return LLA_OK;
+  if (!cache_apart(p.cache)) return LLA_ERR_SHAPE;
+  if (!p.x_k || !p.x_v) return LLA_ERR_NULL;
+  if ((st = check_rows(p.x_k, p.dtype, p.x_stride_b, p.x_stride_n, p.x_stride_h)) != LLA_OK) return st;
+  return aligned(p.x_v, 16) ? LLA_OK : LLA_ERR_ALIGN;
+}
+
+int check_kv8_attn(const lla_kv8_attn_params& p) {
+  int st = check_cache(p.cache);
+  if (st != LLA_OK) return st;
+  if (!dtype_ok(p.dtype) || (p.win_k && !dtype_ok(p.win_dtype))) return LLA_ERR_DTYPE;
+  if (p.nq < 0 || p.G < 1) return LLA_ERR_SHAPE;
+  if ((int64_t)p.nq * p.G > 65535) return LLA_ERR_UNSUPPORTED;
+  if ((st = check_i32(p.len)) != LLA_OK) return st;
+  if (!p.len.at && (p.len.all < 0 || p.len.all > p.cache.Ncap)) return LLA_ERR_SHAPE;
+  if (!std::isfinite(p.scale) || p.scale < 0.f) return LLA_ERR_SHAPE;
+  if (p.cache.B == 0 || p.nq == 0) return LLA_OK;
+  if (!p.q || !p.out || (!p.win_k) != (!p.win_v)) return LLA_ERR_NULL;
+  const int64_t row = (int64_t)p.cache.H * p.G * p.cache.d;
+  if ((st = check_rows(p.q, p.dtype, p.q_stride_b, p.q_stride_n, 0)) != LLA_OK) return st;
+  if ((st = check_rows(p.out, p.dtype, p.out_stride_b, p.out_stride_n, 0)) != LLA_OK) return st;
+  // queries may be broadcast (stride 0), outputs may not
+  if (!apart(p.cache.B, p.out_stride_b, p.nq, p.out_stride_n, row)) return LLA_ERR_SHAPE;
+  if (p.q == p.out) return LLA_ERR_UNSUPPORTED;
+  if (p.win_k) {
+    if (p.Wcap < 1) return LLA_ERR_SHAPE;
+    if ((st = check_i32(p.ctx)) != LLA_OK || (st = check_i32(p.tail)) != LLA_OK) return st;
+    if (!p.tail.at && (p.tail.all < 0 || p.tail.all > p.Wcap)) return LLA_ERR_SHAPE;
+    if (!p.ctx.at && p.ctx.all < 0) return LLA_ERR_SHAPE;
+    if ((st = check_rows(p.win_k, p.win_dtype, p.win_stride_b, p.win_stride_n, p.win_stride_h)) != LLA_OK) return st;
+    if (!aligned(p.win_v, 16)) return LLA_ERR_ALIGN;
+  }
+  if (p.weights) {
+    if (!aligned(p.weights, 4)) return LLA_ERR_ALIGN;
+    if (!apart(p.cache.B, p.weights_stride_b, p.cache.H, p.weights_stride_h, p.cache.Ncap)) return LLA_ERR_SHAPE;
+  }
+  return LLA_OK;
+}
+
+struct Kv8AttnPlan {
+  size_t o_ml, bytes;
+};
+
+Kv8AttnPlan plan_kv8_attn(const lla_kv8_attn_params& p) {
+  Kv8AttnPlan pl;
+  Carve c;
+  pl.o_ml = c.take(p.weights ? (size_t)p.cache.B * p.cache.H * p.nq * p.G * sizeof(float2) : 0);
+  pl.bytes = c.off;
+  return pl;
+}
+
+constexpr int kMaxEvictBlocks = 8192;   // of a head: the selection holds a key of each in shared memory
+
+int check_kv8_evict(const lla_kv8_evict_params& p) {
+  int st = check_cache(p.src);
+  if (st == LLA_OK) st = check_cache(p.dst);
+  if (st != LLA_OK) return st;
+  if (p.src.B != p.dst.B || p.src.H != p.dst.H || p.src.d != p.dst.d || p.src.block != p.dst.block)
+    return LLA_ERR_SHAPE;
+  if (p.src.code != p.dst.code) return LLA_ERR_DTYPE;
+  if (p.first < 0 || p.last < 1 || p.keep < 1 || (int64_t)p.first + p.last > p.keep) return LLA_ERR_SHAPE;
+  if (p.keep > p.src.Ncap / p.src.block || p.keep > p.dst.Ncap / p.dst.block) return LLA_ERR_SHAPE;
+  if (p.src.Ncap / p.src.block > kMaxEvictBlocks || p.src.B > 65535) return LLA_ERR_UNSUPPORTED;
+  if (p.src.B == 0) return LLA_OK;
+  if (!p.weights || !p.dst_weights || !p.len || !p.dst_len) return LLA_ERR_NULL;
+  if (!aligned(p.weights, 4) || !aligned(p.dst_weights, 4) || !aligned(p.len, 4) || !aligned(p.dst_len, 4) ||
+      (p.kept && !aligned(p.kept, 4)))
+    return LLA_ERR_ALIGN;
+  if (p.weights_stride_b < 0 || p.weights_stride_h < 0) return LLA_ERR_SHAPE;
+  if (!cache_apart(p.dst) ||
+      !apart(p.dst.B, p.dst_weights_stride_b, p.dst.H, p.dst_weights_stride_h, p.dst.Ncap))
+    return LLA_ERR_SHAPE;
+  // in place: every plane is the source's, with its strides; otherwise none is
+  const lla_kv8_cache &s = p.src, &d = p.dst;
+  const int same = (s.k == d.k) + (s.v == d.v) + (s.k_scale == d.k_scale) + (s.v_scale == d.v_scale) +
+                   (p.weights == p.dst_weights);
+  if (same != 0 && same != 5) return LLA_ERR_UNSUPPORTED;
+  if (same == 5 && (s.Ncap != d.Ncap || s.stride_b != d.stride_b || s.stride_h != d.stride_h || s.scale_stride_b != d.scale_stride_b ||
+                    s.scale_stride_h != d.scale_stride_h || p.weights_stride_b != p.dst_weights_stride_b ||
+                    p.weights_stride_h != p.dst_weights_stride_h))
+    return LLA_ERR_UNSUPPORTED;
+  return LLA_OK;
+}
+
+struct Kv8EvictPlan {
+  size_t o_kept, o_info, bytes;
+};
+
+Kv8EvictPlan plan_kv8_evict(const lla_kv8_evict_params& p) {
+  Kv8EvictPlan pl;
+  Carve c;
+  pl.o_kept = c.take(p.kept ? 0 : (size_t)p.src.B * p.src.H * p.keep * sizeof(int));
+  pl.o_info = c.take((size_t)p.src.B * sizeof(int2));
+  pl.bytes = c.off;
+  return pl;
+}
+
 int ws_ok(void* ws, size_t ws_bytes, size_t need) {
   if (need == 0) return LLA_OK;
   if (!ws || !aligned(ws, kAlign) || ws_bytes < need) return LLA_ERR_WORKSPACE;
@@ -546,6 +696,58 @@ int lla_decode_attn(const lla_decode_params* p, void* ws, size_t ws_bytes, lla_s
     e = launch_merge(g, s);
   }
   return cuda_status(e);
+}
+
+int lla_kv8_write(const lla_kv8_write_params* p, lla_stream stream) {
+  if (!p) return LLA_ERR_NULL;
+  const int st = check_kv8_write(*p);
+  if (st != LLA_OK) return st;
+  if (p->cache.B == 0 || p->max_n == 0) return LLA_OK;
+  return cuda_status(launch_kv8_write(*p, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t lla_kv8_attn_workspace_bytes(const lla_kv8_attn_params* p) {
+  if (!p || check_kv8_attn(*p) != LLA_OK || p->cache.B == 0 || p->nq == 0) return 0;
+  return plan_kv8_attn(*p).bytes;
+}
+
+int lla_kv8_attn(const lla_kv8_attn_params* p, void* ws, size_t ws_bytes, lla_stream stream) {
+  if (!p) return LLA_ERR_NULL;
+  int st = check_kv8_attn(*p);
+  if (st != LLA_OK) return st;
+  if (p->cache.B == 0 || p->nq == 0) return LLA_OK;
+  const Kv8AttnPlan pl = plan_kv8_attn(*p);
+  st = ws_ok(ws, ws_bytes, pl.bytes);
+  if (st != LLA_OK) return st;
+  Kv8AttnArgs a;
+  std::memset(&a, 0, sizeof(a));
+  a.p = *p;
+  a.rows = p->nq * p->G;
+  a.qmul = (p->scale > 0.f ? p->scale : 1.0f / std::sqrt((float)p->cache.d)) * kLog2e;
+  a.ml = p->weights ? reinterpret_cast<float2*>(static_cast<char*>(ws) + pl.o_ml) : nullptr;
+  return cuda_status(launch_kv8_attn(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t lla_kv8_evict_workspace_bytes(const lla_kv8_evict_params* p) {
+  if (!p || check_kv8_evict(*p) != LLA_OK || p->src.B == 0) return 0;
+  return plan_kv8_evict(*p).bytes;
+}
+
+int lla_kv8_evict(const lla_kv8_evict_params* p, void* ws, size_t ws_bytes, lla_stream stream) {
+  if (!p) return LLA_ERR_NULL;
+  int st = check_kv8_evict(*p);
+  if (st != LLA_OK) return st;
+  if (p->src.B == 0) return LLA_OK;
+  const Kv8EvictPlan pl = plan_kv8_evict(*p);
+  st = ws_ok(ws, ws_bytes, pl.bytes);
+  if (st != LLA_OK) return st;
+  Kv8EvictArgs a;
+  std::memset(&a, 0, sizeof(a));
+  a.p = *p;
+  a.inplace = p->src.k == p->dst.k;
+  a.kept = p->kept ? p->kept : reinterpret_cast<int*>(static_cast<char*>(ws) + pl.o_kept);
+  a.info = reinterpret_cast<int2*>(static_cast<char*>(ws) + pl.o_info);
+  return cuda_status(launch_kv8_evict(a, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -201,4 +201,26 @@ int absorb_tc_rows_pad(int rows);
 int absorb_tc_splits(int B, int n_lat, int num_sms);
 cudaError_t launch_absorb_split_tc(const AbsorbArgs& a, cudaStream_t st);
 
+// ------------------------------------------------- 8-bit K/V cache (kv8) --
+// Per-sequence value: at[b], or all.
+__device__ __forceinline__ int kv8_at(const lla_i32& v, int b) { return v.at ? v.at[b] : v.all; }
+
+cudaError_t launch_kv8_write(const lla_kv8_write_params& p, cudaStream_t st);
+
+struct Kv8AttnArgs {
+  lla_kv8_attn_params p;
+  int rows;                // nq * G query rows of a head
+  float qmul;              // scale * log2(e)
+  float2* ml;              // [B][H][rows] running maximum (base-2 exponent) and sum
+};
+cudaError_t launch_kv8_attn(const Kv8AttnArgs& a, cudaStream_t st);
+
+struct Kv8EvictArgs {
+  lla_kv8_evict_params p;
+  int inplace;
+  int* kept;               // [B][H][keep]
+  int2* info;              // [B] old and new length
+};
+cudaError_t launch_kv8_evict(const Kv8EvictArgs& a, cudaStream_t st);
+
 }  // namespace lla
