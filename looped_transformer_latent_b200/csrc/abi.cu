@@ -402,14 +402,49 @@ int check_kv8_attn(const lla_kv8_attn_params& p) {
 }
 
 struct Kv8AttnPlan {
-  size_t o_ml, bytes;
+  int rows_pass, nt, S, tps, ST, tpc;
+  size_t o_ml, o_y, o_scores, bytes;
 };
+
+// Rows go to CTAs in tiles of 8, 16 or 32.  Cached tokens are split so that a
+// few waves of CTAs cover uneven lengths, but not below 128 tokens (a step of
+// each warp) nor 16 a row (a split's partial output is 8 d bytes a row written
+// and read, its codes 2 d bytes a token).  With weights the scores of a pass
+// are kept; more rows than fit kScoreBytes go in several passes.
+constexpr size_t kScoreBytes = (size_t)256 << 20;
 
 Kv8AttnPlan plan_kv8_attn(const lla_kv8_attn_params& p) {
   Kv8AttnPlan pl;
-  Carve c;
-  pl.o_ml = c.take(p.weights ? (size_t)p.cache.B * p.cache.H * p.nq * p.G * sizeof(float2) : 0);
-  pl.bytes = c.off;
+  const lla_kv8_cache& c = p.cache;
+  const int64_t bh = (int64_t)c.B * c.H;
+  const int rows = p.nq * p.G;
+  pl.rows_pass = rows;
+  if (p.weights && c.Ncap > 0) {
+    const int64_t fit = (int64_t)(kScoreBytes / sizeof(float)) / (bh * c.Ncap) / 32 * 32;
+    pl.rows_pass = (int)std::min<int64_t>(rows, std::max<int64_t>(fit, 32));
+  }
+  // 32 rows of more than 128 elements do not fit a thread's registers
+  pl.nt = pl.rows_pass <= 8 ? 1 : pl.rows_pass <= 16 || c.d > 128 ? 2 : 4;
+  const int tiles = ceil_div(pl.rows_pass, 8 * pl.nt);
+  pl.S = 0; pl.tps = 0;
+  const int most = p.len.at ? c.Ncap : p.len.all;
+  if (most > 0) {
+    const int64_t ctas = bh * tiles, target = (int64_t)num_sms() * 3 * 4;
+    const int least = std::max(128, 16 * std::min(pl.rows_pass, 8 * pl.nt));
+    int64_t S = std::max<int64_t>(1, (target + ctas - 1) / ctas);
+    S = std::min<int64_t>(S, ceil_div(most, least));
+    pl.tps = (int)(((most + S - 1) / S + 127) / 128 * 128);
+    pl.S = ceil_div(most, pl.tps);
+  }
+  pl.tpc = 64;
+  const int tail = !p.win_k ? 0 : p.tail.at ? p.Wcap : p.tail.all;
+  pl.ST = pl.S + ceil_div(tail, pl.tpc);
+  Carve v;
+  const size_t parts = (size_t)bh * pl.rows_pass * pl.ST;
+  pl.o_ml = v.take(parts * sizeof(float2));
+  pl.o_y = v.take(parts * c.d * sizeof(float));
+  pl.o_scores = v.take(p.weights ? (size_t)bh * pl.rows_pass * c.Ncap * sizeof(float) : 0);
+  pl.bytes = v.off;
   return pl;
 }
 
@@ -723,8 +758,12 @@ int lla_kv8_attn(const lla_kv8_attn_params* p, void* ws, size_t ws_bytes, lla_st
   std::memset(&a, 0, sizeof(a));
   a.p = *p;
   a.rows = p->nq * p->G;
+  a.rows_pass = pl.rows_pass; a.nt = pl.nt; a.S = pl.S; a.tps = pl.tps; a.ST = pl.ST; a.tpc = pl.tpc;
   a.qmul = (p->scale > 0.f ? p->scale : 1.0f / std::sqrt((float)p->cache.d)) * kLog2e;
-  a.ml = p->weights ? reinterpret_cast<float2*>(static_cast<char*>(ws) + pl.o_ml) : nullptr;
+  char* w = static_cast<char*>(ws);
+  a.part_ml = reinterpret_cast<float2*>(w + pl.o_ml);
+  a.part_y = reinterpret_cast<float*>(w + pl.o_y);
+  a.scores = p->weights ? reinterpret_cast<float*>(w + pl.o_scores) : nullptr;
   return cuda_status(launch_kv8_attn(a, reinterpret_cast<cudaStream_t>(stream)));
 }
 

@@ -209,9 +209,15 @@ cudaError_t launch_kv8_write(const lla_kv8_write_params& p, cudaStream_t st);
 
 struct Kv8AttnArgs {
   lla_kv8_attn_params p;
-  int rows;                // nq * G query rows of a head
   float qmul;              // scale * log2(e)
-  float2* ml;              // [B][H][rows] running maximum (base-2 exponent) and sum
+  int rows, row0;          // query rows of a head (nq * G) that a launch serves, the first of them
+  int rows_pass;           // most rows of one launch
+  int nt;                  // row tiles of 8 that a CTA serves
+  int S, tps;              // splits of the cached tokens, tokens of each
+  int ST, tpc;             // all splits: S, then those of the exact tokens, tpc tokens each
+  float2* part_ml;         // [B][H][rows][ST] running maximum (base-2 exponent) and sum
+  float* part_y;           // [B][H][rows][ST][d]
+  float* scores;           // [B][H][rows][Ncap] base-2 logits of the cached tokens (weights only), or null
 };
 cudaError_t launch_kv8_attn(const Kv8AttnArgs& a, cudaStream_t st);
 
