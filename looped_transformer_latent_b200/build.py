@@ -18,7 +18,8 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "liblla.so")
 
 SOURCES = ["abi.cu", "writer.cu", "decode_simt.cu", "decode_tc.cu", "decode_fp8.cu", "maps.cu", "gemm_tc.cu",
-           "recon_tc.cu", "noalloc.cu", "kv8.cu", "kv8_attn.cu"]
+           "recon_tc.cu", "noalloc.cu", "kv8.cu", "kv8_attn.cu",
+           "kv8_attn_i8_bf16.cu", "kv8_attn_i8_f32.cu", "kv8_attn_e4m3_bf16.cu", "kv8_attn_e4m3_f32.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 
@@ -54,7 +55,7 @@ def build(force=False, verbose=False):
     srcs, _ = _inputs()
     tmp = LIB + ".tmp"
     cmd = [nvcc_path(), *ARCH, "-O3", "-lineinfo", "-std=c++17",
-           "-Xcompiler", "-fPIC", "-shared", "-I", INCLUDE, "-I", CSRC,
+           "-Xcompiler", "-fPIC", "-shared", "--threads", "0", "-I", INCLUDE, "-I", CSRC,
            *srcs, "-o", tmp]
     if verbose:
         cmd.insert(1, "-Xptxas=-v")

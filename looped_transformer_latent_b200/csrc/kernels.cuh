@@ -220,6 +220,11 @@ struct Kv8AttnArgs {
   float* scores;           // [B][H][rows][Ncap] base-2 logits of the cached tokens (weights only), or null
 };
 cudaError_t launch_kv8_attn(const Kv8AttnArgs& a, cudaStream_t st);
+// the split kernel of one code format and query type
+cudaError_t launch_kv8_attn_i8_bf16(const Kv8AttnArgs& a, cudaStream_t st);
+cudaError_t launch_kv8_attn_i8_f32(const Kv8AttnArgs& a, cudaStream_t st);
+cudaError_t launch_kv8_attn_e4m3_bf16(const Kv8AttnArgs& a, cudaStream_t st);
+cudaError_t launch_kv8_attn_e4m3_f32(const Kv8AttnArgs& a, cudaStream_t st);
 
 struct Kv8EvictArgs {
   lla_kv8_evict_params p;

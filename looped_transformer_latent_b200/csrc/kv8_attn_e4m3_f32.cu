@@ -1,0 +1,6 @@
+// Attention over a cache of e4m3 codes, float32 queries and outputs.
+#include "kv8_attn.cuh"
+
+namespace lla {
+cudaError_t launch_kv8_attn_e4m3_f32(const Kv8AttnArgs& a, cudaStream_t st) { return kv8::launch_d<LLA_KV8_E4M3, 2>(a, st); }
+}  // namespace lla
