@@ -406,10 +406,11 @@ struct Kv8AttnPlan {
   size_t o_ml, o_y, o_scores, bytes;
 };
 
-// Rows go to CTAs in tiles of 8, 16 or 32.  Cached tokens are split so that a
-// few waves of CTAs cover uneven lengths, but not below 128 tokens (a step of
-// each warp) nor 16 a row (a split's partial output is 8 d bytes a row written
-// and read, its codes 2 d bytes a token).  With weights the scores of a pass
+// Rows go to CTAs in tiles of 8, 16 or 32.  Cached tokens are split so that the
+// time is least by this count: the CTAs that the fullest SM gets share its
+// bandwidth, one wave takes at least half of what its CTAs would take in turn,
+// and a CTA costs some tokens' worth besides its own.  Never below 128 tokens
+// (a step or two of each warp).  With weights the scores of a pass
 // are kept; more rows than fit kScoreBytes go in several passes.
 constexpr size_t kScoreBytes = (size_t)256 << 20;
 
@@ -423,24 +424,30 @@ Kv8AttnPlan plan_kv8_attn(const lla_kv8_attn_params& p) {
     const int64_t fit = (int64_t)(kScoreBytes / sizeof(float)) / (bh * c.Ncap) / 32 * 32;
     pl.rows_pass = (int)std::min<int64_t>(rows, std::max<int64_t>(fit, 32));
   }
-  // 32 rows of more than 128 elements do not fit a thread's registers
-  pl.nt = pl.rows_pass <= 8 ? 1 : pl.rows_pass <= 16 || c.d > 128 ? 2 : 4;
+  // 32 rows of more than 128 elements, or with two terms of each, do not fit a thread's registers
+  const bool f32 = p.dtype == LLA_F32;
+  pl.nt = pl.rows_pass <= 8 ? 1 : pl.rows_pass <= 16 || c.d > 128 || c.block < 32 || f32 ? 2 : 4;
   const int tiles = ceil_div(pl.rows_pass, 8 * pl.nt);
   pl.S = 0; pl.tps = 0;
   const int most = p.len.at ? c.Ncap : p.len.all;
   if (most > 0) {
-    const int64_t ctas = bh * tiles, target = (int64_t)num_sms() * 3 * 4;
-    const int least = std::max(128, 16 * std::min(pl.rows_pass, 8 * pl.nt));
-    int64_t S = std::max<int64_t>(1, (target + ctas - 1) / ctas);
-    S = std::min<int64_t>(S, ceil_div(most, least));
-    pl.tps = (int)(((most + S - 1) / S + 127) / 128 * 128);
+    const int64_t ctas = bh * tiles, sms = num_sms(), per_sm = kv8_ctas_per_sm(c.d, pl.nt, f32 ? 2 : 1);
+    const int64_t extra = 48 + 24 * pl.nt;       // tokens' worth of queries, join and partial results
+    int64_t best = INT64_MAX;
+    for (int S = 1; S <= ceil_div(most, 128) && S <= 512; ++S) {
+      const int tps = (most + S - 1) / S + 127 & ~127;
+      const int64_t n = ctas * ceil_div(most, tps);
+      const int64_t shared = 2 * ((n + sms - 1) / sms), alone = per_sm * ((n + sms * per_sm - 1) / (sms * per_sm));
+      const int64_t cost = std::max(shared, alone) * (tps + extra);
+      if (cost < best) { best = cost; pl.tps = tps; }
+    }
     pl.S = ceil_div(most, pl.tps);
   }
   pl.tpc = 64;
   const int tail = !p.win_k ? 0 : p.tail.at ? p.Wcap : p.tail.all;
   pl.ST = pl.S + ceil_div(tail, pl.tpc);
   Carve v;
-  const size_t parts = (size_t)bh * pl.rows_pass * pl.ST;
+  const size_t parts = pl.ST == 1 && !p.weights ? 0 : (size_t)bh * pl.rows_pass * pl.ST;
   pl.o_ml = v.take(parts * sizeof(float2));
   pl.o_y = v.take(parts * c.d * sizeof(float));
   pl.o_scores = v.take(p.weights ? (size_t)bh * pl.rows_pass * c.Ncap * sizeof(float) : 0);
@@ -759,6 +766,7 @@ int lla_kv8_attn(const lla_kv8_attn_params* p, void* ws, size_t ws_bytes, lla_st
   a.p = *p;
   a.rows = p->nq * p->G;
   a.rows_pass = pl.rows_pass; a.nt = pl.nt; a.S = pl.S; a.tps = pl.tps; a.ST = pl.ST; a.tpc = pl.tpc;
+  a.direct = pl.ST == 1 && !p->weights;
   a.qmul = (p->scale > 0.f ? p->scale : 1.0f / std::sqrt((float)p->cache.d)) * kLog2e;
   char* w = static_cast<char*>(ws);
   a.part_ml = reinterpret_cast<float2*>(w + pl.o_ml);

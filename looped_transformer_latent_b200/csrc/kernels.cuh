@@ -205,6 +205,19 @@ cudaError_t launch_absorb_split_tc(const AbsorbArgs& a, cudaStream_t st);
 // Per-sequence value: at[b], or all.
 __device__ __forceinline__ int kv8_at(const lla_i32& v, int b) { return v.at ? v.at[b] : v.all; }
 
+// 4 elements times inv at element offset `at`
+__device__ __forceinline__ void store_quad(void* out, int64_t at, int dtype, float4 s, float inv) {
+  if (dtype == LLA_BF16) {
+    const __nv_bfloat162 a = __floats2bfloat162_rn(s.x * inv, s.y * inv), b = __floats2bfloat162_rn(s.z * inv, s.w * inv);
+    uint2 v;
+    v.x = *reinterpret_cast<const uint32_t*>(&a);
+    v.y = *reinterpret_cast<const uint32_t*>(&b);
+    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(out) + at) = v;
+  } else {
+    *reinterpret_cast<float4*>(static_cast<float*>(out) + at) = make_float4(s.x * inv, s.y * inv, s.z * inv, s.w * inv);
+  }
+}
+
 cudaError_t launch_kv8_write(const lla_kv8_write_params& p, cudaStream_t st);
 
 struct Kv8AttnArgs {
@@ -215,11 +228,17 @@ struct Kv8AttnArgs {
   int nt;                  // row tiles of 8 that a CTA serves
   int S, tps;              // splits of the cached tokens, tokens of each
   int ST, tpc;             // all splits: S, then those of the exact tokens, tpc tokens each
+  int direct;              // one split and no weights: the split kernel writes the outputs itself
   float2* part_ml;         // [B][H][rows][ST] running maximum (base-2 exponent) and sum
   float* part_y;           // [B][H][rows][ST][d]
   float* scores;           // [B][H][rows][Ncap] base-2 logits of the cached tokens (weights only), or null
 };
 cudaError_t launch_kv8_attn(const Kv8AttnArgs& a, cudaStream_t st);
+// CTAs of the split kernel that an SM holds, by head dim, row tiles and query
+// terms (fp32: 2): what registers and shared memory allow
+__host__ __device__ constexpr int kv8_ctas_per_sm(int d, int nt, int terms) {
+  return d > 128 ? (nt == 1 ? 2 : 1) : nt == 1 ? 4 : nt == 2 && terms == 1 ? 3 : 2;
+}
 // the split kernel of one code format and query type
 cudaError_t launch_kv8_attn_i8_bf16(const Kv8AttnArgs& a, cudaStream_t st);
 cudaError_t launch_kv8_attn_i8_f32(const Kv8AttnArgs& a, cudaStream_t st);

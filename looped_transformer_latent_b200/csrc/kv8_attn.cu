@@ -24,36 +24,70 @@ __device__ __forceinline__ float2 row_ml(const float2* ml, int ST) {
 
 constexpr int JT = 512;          // cached tokens of a weights CTA
 
-// CTAs below `joins` write the outputs, a warp for each row; the others add a
-// stretch of the head's weights: each token's terms over the rows in order.
-__global__ void __launch_bounds__(AT) kv8_join_kernel(const Kv8AttnArgs a, int joins) {
+// Sum of a row's splits [i0, ST) in steps of `step`, by one warp; a lane holds 4 elements.
+// Loads of 8 splits are under way at a time; an empty split's y is not there.
+__device__ __forceinline__ float4 row_sum(const float2* ml, const float* y, int ST, int d, int e, float m, int i0, int step) {
+  const int lane = threadIdx.x & 31;
+  float4 s = make_float4(0, 0, 0, 0);
+  for (int base = i0; base < ST; base += 32 * step) {
+    const int mine = base + lane * step;
+    const float2 x = mine < ST ? ml[mine] : make_float2(-INFINITY, 0.f);
+    const bool there = !(x.x == -INFINITY && x.y == 0.f);
+    const float f = there ? exp2f(x.x - m) : 0.f;
+    const unsigned some = __ballot_sync(0xffffffffu, there);
+    const int n = min(32, (ST - base + step - 1) / step);
+    for (int k0 = 0; k0 < n; k0 += 8) {
+      float4 v[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        v[k] = e < d && (some >> (k0 + k) & 1) ? *reinterpret_cast<const float4*>(y + (int64_t)(base + (k0 + k) * step) * d + e)
+                                               : make_float4(0, 0, 0, 0);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float g = __shfl_sync(0xffffffffu, f, k0 + k);
+        s.x += g * v[k].x; s.y += g * v[k].y; s.z += g * v[k].z; s.w += g * v[k].w;
+      }
+    }
+  }
+  return s;
+}
+
+// CTAs below `joins` write the outputs, a warp (a.wide: a CTA) for each row;
+// the others add a stretch of the head's weights: each token's terms over the
+// rows in order.
+__global__ void __launch_bounds__(AT) kv8_join_kernel(const __grid_constant__ Kv8AttnArgs a, int joins, int wide) {
   __shared__ float2 sml[32];
+  __shared__ float4 sy[AW][64];
   griddep_wait();
   const lla_kv8_attn_params& p = a.p;
   const lla_kv8_cache& c = p.cache;
   const int h = blockIdx.y, b = blockIdx.z, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t bh = (int64_t)b * c.H + h;
   if ((int)blockIdx.x < joins) {
-    const int r = blockIdx.x * AW + warp;
+    const int r = wide ? blockIdx.x : blockIdx.x * AW + warp;
     if (r >= a.rows) return;
     const float2* ml = a.part_ml + (bh * a.rows + r) * a.ST;
     const float2 all = row_ml(ml, a.ST);
     const float* y = a.part_y + (bh * a.rows + r) * a.ST * c.d;
     const int row = a.row0 + r, qp = row / p.G, gq = row % p.G;
     const int64_t o = (int64_t)b * p.out_stride_b + (int64_t)qp * p.out_stride_n + (int64_t)(h * p.G + gq) * c.d;
-    for (int e = 4 * lane; e < c.d; e += 128) {
-      float4 s = make_float4(0, 0, 0, 0);
-      for (int i = 0; i < a.ST; ++i) {
-        const float2 x = ml[i];
-        if (x.x == -INFINITY && x.y == 0.f) continue;     // an empty split wrote no y
-        const float f = exp2f(x.x - all.x);
-        const float4 v = *reinterpret_cast<const float4*>(y + (int64_t)i * c.d + e);
-        s.x += f * v.x; s.y += f * v.y; s.z += f * v.z; s.w += f * v.w;
+    for (int e0 = 0; e0 < c.d; e0 += 128) {
+      const int e = e0 + 4 * lane;
+      float4 s = row_sum(ml, y, a.ST, c.d, e, all.x, wide ? warp : 0, wide ? AW : 1);
+      if (wide) sy[warp][e / 4] = s;
+      else if (e < c.d) store_quad(p.out, o + e, p.dtype, s, all.y);
+    }
+    if (!wide) return;
+    __syncthreads();
+    const int e = 4 * threadIdx.x;
+    if (e < c.d) {
+      float4 s = sy[0][e / 4];
+#pragma unroll
+      for (int w = 1; w < AW; ++w) {
+        const float4 v = sy[w][e / 4];
+        s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
       }
-      store_elem(p.out, o + e, p.dtype, s.x * all.y);
-      store_elem(p.out, o + e + 1, p.dtype, s.y * all.y);
-      store_elem(p.out, o + e + 2, p.dtype, s.z * all.y);
-      store_elem(p.out, o + e + 3, p.dtype, s.w * all.y);
+      store_quad(p.out, o + e, p.dtype, s, all.y);
     }
     return;
   }
@@ -103,9 +137,11 @@ cudaError_t launch_kv8_attn(const Kv8AttnArgs& a0, cudaStream_t st) {
       else e = f32 ? launch_kv8_attn_e4m3_f32(a, st) : launch_kv8_attn_e4m3_bf16(a, st);
     }
     if (e != cudaSuccess) return e;
-    const int joins = ceil_div(a.rows, AW);
+    if (a.direct) continue;
+    const int wide = a.ST >= 8;                  // many splits: a CTA for each row shortens the chain of loads
+    const int joins = wide ? a.rows : ceil_div(a.rows, AW);
     e = launch_kernel(kv8_join_kernel, dim3(joins + (a.p.weights ? ceil_div(c.Ncap, JT) : 0), c.H, c.B), dim3(AT), 0, st,
-                      1, a, joins);
+                      1, a, joins, wide);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;

@@ -110,6 +110,14 @@ __device__ __forceinline__ void split_bf16(float x, float y, uint32_t (&o)[T]) {
     x -= u.x; y -= u.y;
   }
 }
+// 2^x; below 2^-126 it is 0
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+// 2^e, -126 <= e <= 127
+__device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }
 // 8 x 8 transpose across the warp: lane (g, t) of (row g, columns 2t, 2t + 1)
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   uint32_t r;
@@ -186,19 +194,20 @@ __device__ __forceinline__ void read_row(uint32_t* w, uint32_t base, int r, int 
 // next 11 bits of an fp32 one.
 constexpr int kQExp = 13;
 // Running references of a row, both base-2 exponents: m of the probabilities
-// p = exp2(s - m), a of what meets the value codes, w = exp2(s + log2(scale) - a),
+// p = exp2(s - m), a of what meets the value codes, w = 2^12 exp2(s + log2(scale) - a),
 // so that a block whose values are 2^60 times another's does not drown it.  A
-// reference is set kOff below a new maximum and follows it only when it is
-// exceeded by kSlack more: w stays below 2^12 in f16, the largest above 2^-8,
-// and most tiles need neither a shuffle nor a rescaling.
-constexpr float kOff = 4.f, kSlack = 12.f, kUnset = -1e30f;
+// reference is set kSlack above a new maximum and moves only when a logit
+// exceeds it: p <= 1, w <= 2^12 in f16 and the largest of them above 2^-4, and
+// most tiles need neither a shuffle nor a rescaling.
+constexpr float kSlack = 12.f, kUnset = -1e30f;
 
-constexpr int STAGES = 3;        // tiles of a warp's ring: one in use, two on their way
 
-template <int D, int NT>
+// MT: tiles of 16 tokens that a warp takes at a time.
+template <int D, int NT, int MT>
 struct Smem {
   static constexpr int RT = 8 * NT;
-  static constexpr int tile = 16 * Row<D>::pitch;                     // bytes of 16 rows
+  static constexpr int STAGES = MT == 1 ? 3 : 2;                      // of a warp's ring, one of them in use
+  static constexpr int tile = 16 * MT * Row<D>::pitch;                // bytes of a stage's rows
   uint2 q[3][D / 16][NT][32];    // query terms, B operand order
   float rowf[RT];                // row exponent times scale log2(e)
   float2 ml[2][RT];              // join of the warps
@@ -226,12 +235,16 @@ struct Place {
     const int row = a.row0 + row0 + r, qp = row / a.p.G, gq = row % a.p.G;
     return (int64_t)b * a.p.q_stride_b + (int64_t)qp * a.p.q_stride_n + (int64_t)(h * a.p.G + gq) * a.p.cache.d;
   }
+  __device__ int64_t output(const Kv8AttnArgs& a, int r) const {      // and of its output
+    const int row = a.row0 + row0 + r, qp = row / a.p.G, gq = row % a.p.G;
+    return (int64_t)b * a.p.out_stride_b + (int64_t)qp * a.p.out_stride_n + (int64_t)(h * a.p.G + gq) * a.p.cache.d;
+  }
 };
 
 // Join of the warps, 3 -> 1 and 2 -> 0, then 1 -> 0, and the split's partial
 // results.  acc, l in units of exp2(m); base(w): first element of quad w.
-template <int D, int NT, class Base>
-__device__ __forceinline__ void join_store(const Kv8AttnArgs& a, Smem<D, NT>& sm, const Place& at_, float (&acc)[D / 16][NT][4],
+template <int D, int NT, int MT, class Base>
+__device__ __forceinline__ void join_store(const Kv8AttnArgs& a, Smem<D, NT, MT>& sm, const Place& at_, float (&acc)[D / 16][NT][4],
                                            float (&m)[2 * NT], float (&l)[2 * NT], Base base) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
 #pragma unroll
@@ -277,6 +290,16 @@ __device__ __forceinline__ void join_store(const Kv8AttnArgs& a, Smem<D, NT>& sm
     for (int e = 0; e < 2; ++e) {
       const int r = at_.row0 + 8 * n + 2 * t + e;
       if (r >= a.rows) continue;
+      if (a.direct) {                            // the only split: these are the sums
+        const float inv = l[2 * n + e] == 0.f ? 0.f : 1.f / l[2 * n + e];
+        const int64_t o = at_.output(a, r - at_.row0);
+#pragma unroll
+        for (int w = 0; w < D / 32; ++w)
+          if (base(w) < d)
+            store_quad(a.p.out, o + base(w), a.p.dtype,
+                       make_float4(acc[2 * w][n][e], acc[2 * w][n][e + 2], acc[2 * w + 1][n][e], acc[2 * w + 1][n][e + 2]), inv);
+        continue;
+      }
       const int64_t at = (at_.bh * a.rows + r) * a.ST + at_.split;
       if (g == 0) a.part_ml[at] = make_float2(m[2 * n + e], l[2 * n + e]);
 #pragma unroll
@@ -289,9 +312,29 @@ __device__ __forceinline__ void join_store(const Kv8AttnArgs& a, Smem<D, NT>& sm
     }
 }
 
+// A quad of 4 query elements.
+__device__ __forceinline__ void load_query(float (&x)[4], const void* q, int64_t at, int dtype, bool ok) {
+  if (dtype == LLA_BF16) {
+    const uint2 v = ok ? __ldg(reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(q) + at)) : make_uint2(0, 0);
+    const float2 a = unpack_bf16(v.x), b = unpack_bf16(v.y);
+    x[0] = a.x; x[1] = a.y; x[2] = b.x; x[3] = b.y;
+  } else {
+    const float4 v = ok ? __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(q) + at)) : make_float4(0, 0, 0, 0);
+    x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
+  }
+}
+
 // Nothing to see in this split: the join must not read what was there.
 template <int RT>
 __device__ __forceinline__ void empty_split(const Kv8AttnArgs& a, const Place& at) {
+  if (a.direct) {
+    for (int i = threadIdx.x; i < RT * (a.p.cache.d / 4); i += AT) {
+      const int r = i / (a.p.cache.d / 4);
+      if (at.row0 + r < a.rows)
+        store_quad(a.p.out, at.output(a, r) + 4 * (i % (a.p.cache.d / 4)), a.p.dtype, make_float4(0, 0, 0, 0), 0.f);
+    }
+    return;
+  }
   if ((int)threadIdx.x < RT && at.row0 + (int)threadIdx.x < a.rows)
     a.part_ml[(at.bh * a.rows + at.row0 + threadIdx.x) * a.ST + at.split] = make_float2(-INFINITY, 0.f);
 }
@@ -322,8 +365,8 @@ __device__ __forceinline__ bool no_number(uint32_t w) {   // of two bf16 (a term
 // WT: terms of the ring's elements (bf16 1, fp32 3).  QT 1: bf16 queries, one
 // exact term, probabilities in two; QT 2: fp32, three of each.  Products of
 // terms whose order exceeds the third are left out: they are below 2^-24.
-template <int D, int NT, int QT, int WT>
-__device__ __noinline__ void exact_split(const Kv8AttnArgs& a, Smem<D, NT>& sm) {
+template <int D, int NT, int MT, int QT, int WT>
+__device__ __noinline__ void exact_split(const Kv8AttnArgs& a, Smem<D, NT, MT>& sm) {
   constexpr int RT = 8 * NT, QB = QT == 1 ? 1 : 3, PB = QT == 1 ? 2 : 3;
   const lla_kv8_attn_params& p = a.p;
   const int d = p.cache.d, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
@@ -340,8 +383,7 @@ __device__ __noinline__ void exact_split(const Kv8AttnArgs& a, Smem<D, NT>& sm) 
   for (int i = threadIdx.x; i < RT * (D / 4); i += AT) {
     const int r = i / (D / 4), w = i % (D / 4) / 4, tt = i % 4, e = quad_k(w, tt);
     float x[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) x[k] = r < rows && e < d ? load_elem(p.q, at.query(a, r) + e + k, p.dtype) : 0.f;
+    load_query(x, p.q, at.query(a, r) + e, p.dtype, r < rows && e < d);
     uint32_t u[QB], v[QB];
     split_bf16<QB>(x[0], x[1], u);
     split_bf16<QB>(x[2], x[3], v);
@@ -411,10 +453,10 @@ __device__ __noinline__ void exact_split(const Kv8AttnArgs& a, Smem<D, NT>& sm) 
         float top = fmaxf(u, v);
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        const float m1 = fmaxf(mo[i], top), f = exp2f(mo[i] - m1);
+        const float m1 = fmaxf(mo[i], top), f = ex2(mo[i] - m1);
         mo[i] = m1;
-        pr[n][e] = tb + g < vis[i] ? exp2f(u - m1) : 0.f;
-        pr[n][e + 2] = tb + g + 8 < vis[i] ? exp2f(v - m1) : 0.f;
+        pr[n][e] = tb + g < vis[i] ? ex2(u - m1) : 0.f;
+        pr[n][e + 2] = tb + g + 8 < vis[i] ? ex2(v - m1) : 0.f;
         l[i] = l[i] * f + (pr[n][e] + pr[n][e + 2]);
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) { acc[k][n][e] *= f; acc[k][n][e + 2] *= f; }
@@ -494,25 +536,25 @@ __device__ __noinline__ void exact_split(const Kv8AttnArgs& a, Smem<D, NT>& sm) 
 #pragma unroll
     for (int o = 4; o < 32; o <<= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], o);
   }
-  join_store<D, NT>(a, sm, at, acc, m, l, [&](int w) { return quad_v<D>(w, g); });
+  join_store<D, NT, MT>(a, sm, at, acc, m, l, [&](int w) { return quad_v<D>(w, g); });
 }
 
 // ----------------------------------------------------------- cached tokens --
-template <int CODE, int D, int NT, int QT>
-__global__ void __launch_bounds__(AT, D > 128 || NT == 4 ? 2 : NT == 2 ? 3 : 4)
+template <int CODE, int D, int NT, int MT, int QT>
+__global__ void __launch_bounds__(AT, kv8_ctas_per_sm(D, NT, QT))
 kv8_attn_kernel(const __grid_constant__ Kv8AttnArgs a) {
-  constexpr int RT = 8 * NT;
+  constexpr int RT = 8 * NT, STEP = 16 * MT, STAGES = Smem<D, NT, MT>::STAGES;
   constexpr int KW = D / 16, VW = D / 32;        // words per lane of a K and of a V row
-  constexpr int PIECES = 16 * (D / 16) / 32;     // 16-byte pieces of a tile that a lane copies
+  constexpr int PIECES = MT * (D / 16) / 2;      // 16-byte pieces of a stage that a lane copies
   using Wd = Widen<CODE>;
   extern __shared__ __align__(128) uint8_t smem_raw[];
-  Smem<D, NT>& sm = *reinterpret_cast<Smem<D, NT>*>(smem_raw);
+  Smem<D, NT, MT>& sm = *reinterpret_cast<Smem<D, NT, MT>*>(smem_raw);
   griddep_wait();
   const lla_kv8_attn_params& p = a.p;
   const lla_kv8_cache& c = p.cache;
   if ((int)blockIdx.x >= a.S) {
-    if (p.win_dtype == LLA_BF16) exact_split<D, NT, QT, 1>(a, sm);
-    else exact_split<D, NT, QT, 3>(a, sm);
+    if (p.win_dtype == LLA_BF16) exact_split<D, NT, MT, QT, 1>(a, sm);
+    else exact_split<D, NT, MT, QT, 3>(a, sm);
     return;
   }
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
@@ -528,61 +570,69 @@ kv8_attn_kernel(const __grid_constant__ Kv8AttnArgs a) {
   const float* vsc = c.v_scale + (int64_t)b * c.scale_stride_b + (int64_t)h * c.scale_stride_h;
   const int bshift = 31 - __clz(c.block);
 
-  // a tile of 16 tokens lies inside one block of the cache; rows past `last` are zeros
-  auto copy_tile = [&](int tb, int stage) {
+  // a step of STEP tokens lies inside one block of the cache; rows past `last` are zeros
+  auto copy_step = [&](int tb, int stage) {
     const uint32_t ks = smem_addr(sm.ring.kv[warp][stage][0]), vs = smem_addr(sm.ring.kv[warp][stage][1]);
+    const uint8_t *kf = kc + (int64_t)tb * c.d, *vf = vc + (int64_t)tb * c.d;
 #pragma unroll
     for (int i = 0; i < PIECES; ++i) {
       const int id = lane + 32 * i, r = id / (D / 16), e = 16 * (id % (D / 16));
       const bool ok = tb + r < last && e < c.d;
-      const int64_t from = ok ? (int64_t)(tb + r) * c.d + e : 0;
-      copy16(ks + Row<D>::at(r, e), kc + from, ok);
-      copy16(vs + Row<D>::at(r, e), vc + from, ok);
+      const int from = ok ? r * c.d + e : 0;
+      copy16(ks + Row<D>::at(r, e), kf + from, ok);
+      copy16(vs + Row<D>::at(r, e), vf + from, ok);
     }
     if (lane < 2) copy4(smem_addr(&sm.ring.scales[warp][stage][lane]), (lane ? vsc : ksc) + (tb >> bshift));
   };
-  int tb = first + 16 * warp;
+  int tb = first + STEP * warp;
 #pragma unroll
   for (int i = 0; i < STAGES - 1; ++i) {
-    if (tb + 16 * AW * i < last) copy_tile(tb + 16 * AW * i, i);
+    if (tb + STEP * AW * i < last) copy_step(tb + STEP * AW * i, i);
     copy_commit();
   }
 
-  // ---- queries: a warp takes RT / 4 rows
+  // ---- queries: a warp takes RT / 4 rows, a lane one or two quads of each
+  constexpr int QL = (D / 4 + 31) / 32;
+#pragma unroll 2
   for (int r = warp; r < RT; r += AW) {
     const bool there = at.row0 + r < a.rows;
     const int64_t qo = at.query(a, r);
-    float top = 0.f;
-    for (int e = lane; e < c.d; e += 32) {
-      const float x = there ? fabsf(load_elem(p.q, qo + e, p.dtype)) : 0.f;
-      top = x > top || x != x ? x : top;         // NaN stays
+    float x[QL][4], top = 0.f;
+#pragma unroll
+    for (int i = 0; i < QL; ++i) {
+      const int id = lane + 32 * i, e = id < D / 4 ? word_at<4>(D, id / 4, id % 4) : D;
+      load_query(x[i], p.q, qo + e, p.dtype, there && e < c.d);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) top = fabsf(x[i][k]) > top || x[i][k] != x[i][k] ? fabsf(x[i][k]) : top;   // NaN stays
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
-      const float x = __shfl_xor_sync(0xffffffffu, top, o);
-      top = x > top || x != x ? x : top;
+      const float u = __shfl_xor_sync(0xffffffffu, top, o);
+      top = u > top || u != u ? u : top;
     }
-    int ex = 0;
-    if (top > 0.f && top < INFINITY) ex = max(ilogbf(top) - kQExp, -100);
-    if (lane == 0) sm.rowf[r] = ldexpf(a.qmul, ex);
-    for (int i = lane; i < KW * 4; i += 32) {    // word w, group lane tt
-      const int w = i / 4, tt = i % 4, e0 = word_at<4>(D, w, tt);
-      float x[4];
+    // ilogb of the largest magnitude (of a subnormal: -127) less kQExp; 0 where that is zero or no number
+    const int ex = top > 0.f && top < INFINITY ? max((__float_as_int(top) >> 23) - 127 - kQExp, -100) : 0;
+    if (lane == 0) sm.rowf[r] = a.qmul * pow2(ex);
+    const float down = pow2(-ex);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) x[e] = there && e0 < c.d ? ldexpf(load_elem(p.q, qo + e0 + e, p.dtype), -ex) : 0.f;
-      uint2 v = make_uint2(pack_f16(x[0], x[1]), pack_f16(x[2], x[3]));
-      sm.q[0][w][r / 8][(r % 8) * 4 + tt] = v;
+    for (int i = 0; i < QL; ++i) {
+      const int id = lane + 32 * i;
+      if (id >= D / 4) break;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) x[i][k] *= down;
+      const uint2 v = make_uint2(pack_f16(x[i][0], x[i][1]), pack_f16(x[i][2], x[i][3]));
+      sm.q[0][id / 4][r / 8][(r % 8) * 4 + id % 4] = v;
       if (QT == 2) {
         const float2 u0 = unpack_f16(v.x), u1 = unpack_f16(v.y);
-        sm.q[1][w][r / 8][(r % 8) * 4 + tt] =
-            make_uint2(pack_f16(x[0] - u0.x, x[1] - u0.y), pack_f16(x[2] - u1.x, x[3] - u1.y));
+        sm.q[1][id / 4][r / 8][(r % 8) * 4 + id % 4] =
+            make_uint2(pack_f16(x[i][0] - u0.x, x[i][1] - u0.y), pack_f16(x[i][2] - u1.x, x[i][3] - u1.y));
       }
     }
   }
   __syncthreads();
 
   float acc[D / 16][NT][4];
-  float mo[2 * NT], ao[2 * NT], F[2 * NT], l[2 * NT];   // references, F = exp2(mo - ao), sums
+  float mo[2 * NT], ao[2 * NT], F[2 * NT], l[2 * NT];   // references, F = 2^12 exp2(mo - ao), sums
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -596,131 +646,167 @@ kv8_attn_kernel(const __grid_constant__ Kv8AttnArgs a) {
   }
 
   int stage = 0;
-  for (; tb < last; tb += 16 * AW) {
-    copy_wait<STAGES - 2>();
-    __syncwarp();                                // every lane's part is there, and the tile before is done with
+  for (; tb < last; tb += STEP * AW) {
+    if (STAGES > 2) copy_wait<STAGES - 2>();
+    else copy_wait<0>();
+    __syncwarp();                                // every lane's part is there, and the step before is done with
     {
-      const int next = tb + 16 * AW * (STAGES - 1), to = stage == 0 ? STAGES - 1 : stage - 1;
-      if (next < last) copy_tile(next, to);
+      const int next = tb + STEP * AW * (STAGES - 1), to = stage == 0 ? STAGES - 1 : stage - 1;
+      if (next < last) copy_step(next, to);
       copy_commit();
     }
     const uint32_t kt = smem_addr(sm.ring.kv[warp][stage][0]), vt = smem_addr(sm.ring.kv[warp][stage][1]);
     const float ks = sm.ring.scales[warp][stage][0], vs = sm.ring.scales[warp][stage][1];
     stage = stage == STAGES - 1 ? 0 : stage + 1;
     // ---- S^T = K q^T
-    float s[NT][4];
+    float s[MT][NT][4];
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+    for (int m = 0; m < MT; ++m)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) s[n][e] = 0.f;
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[m][n][e] = 0.f;
     {
-      uint32_t k0[KW], k1[KW];
-      read_row<4, D>(k0, kt, g, t);
-      read_row<4, D>(k1, kt, g + 8, t);
+      uint32_t k[MT][2][KW];
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        read_row<4, D>(k[m][0], kt, 16 * m + g, t);
+        read_row<4, D>(k[m][1], kt, 16 * m + g + 8, t);
+      }
 #pragma unroll
       for (int w = 0; w < KW; ++w) {
-        const uint32_t x0 = Wd::prep(k0[w]), x1 = Wd::prep(k1[w]);
-        const uint32_t op[4] = {Wd::lo(x0), Wd::lo(x1), Wd::hi(x0), Wd::hi(x1)};
+        uint32_t op[MT][4];
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          const uint32_t x0 = Wd::prep(k[m][0][w]), x1 = Wd::prep(k[m][1][w]);
+          op[m][0] = Wd::lo(x0); op[m][1] = Wd::lo(x1); op[m][2] = Wd::hi(x0); op[m][3] = Wd::hi(x1);
+        }
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
           const uint2 q0 = sm.q[0][w][n][lane];
-          mma_f16(s[n], op, q0.x, q0.y);
+#pragma unroll
+          for (int m = 0; m < MT; ++m) mma_f16(s[m][n], op[m], q0.x, q0.y);
           if (QT == 2) {
             const uint2 q1 = sm.q[1][w][n][lane];
-            mma_f16(s[n], op, q1.x, q1.y);
+#pragma unroll
+            for (int m = 0; m < MT; ++m) mma_f16(s[m][n], op[m], q1.x, q1.y);
           }
         }
       }
     }
-    uint32_t vw[4][VW];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) read_row<8, D>(vw[i], vt, 2 * t + (i & 1) + 8 * (i >> 1), g);
-    // ---- logits (base 2) less their reference; a rise beyond the slack moves the references
+    // ---- logits (base 2); one beyond its reference moves that
     const float lv = __log2f(fabsf(vs));         // of a block of zeros -inf: never a rise
-    const bool whole = tb + 16 <= last, in0 = tb + g < last, in1 = tb + g + 8 < last;
-    float f[2 * NT];
+    const bool whole = tb + STEP <= last;
+    float cv[2 * NT];
     bool rise = false;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       const float2 rf = *reinterpret_cast<const float2*>(&sm.rowf[8 * n + 2 * t]);
-      f[2 * n] = rf.x * ks; f[2 * n + 1] = rf.y * ks;
+      const float f[2] = {rf.x * ks, rf.y * ks};
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const float edge = fminf(mo[2 * n + e], ao[2 * n + e] - lv) + kSlack;
-        rise |= (whole || in0) && s[n][e] * f[2 * n + e] > edge;
-        rise |= (whole || in1) && s[n][e + 2] * f[2 * n + e] > edge;
-      }
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[m][n][e] *= f[e & 1];
+    }
+    if (!whole)
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (tb + 16 * m + g + 8 * (e >> 1) >= last) s[m][n][e] = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < 2 * NT; ++i) {
+      const float edge = fminf(mo[i], ao[i] - lv);
+#pragma unroll
+      for (int m = 0; m < MT; ++m) rise |= fmaxf(s[m][i / 2][i % 2], s[m][i / 2][i % 2 + 2]) > edge;
+      cv[i] = vs * F[i];
+      rise |= cv[i] > 1e30f;                     // kept finite: a probability of 0 may meet it
     }
     if (a.scores) {
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
+      for (int m = 0; m < MT; ++m)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int r = at.row0 + 8 * n + 2 * t + e;
-          if (r >= a.rows) continue;
-          float* to = a.scores + (at.bh * a.rows + r) * c.Ncap + tb + g;
-          if (in0) to[0] = s[n][e] * f[2 * n + e];
-          if (in1) to[8] = s[n][e + 2] * f[2 * n + e];
-        }
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int r = at.row0 + 8 * n + 2 * t + (e & 1), j = tb + 16 * m + g + 8 * (e >> 1);
+            if (r < a.rows && j < last) a.scores[(at.bh * a.rows + r) * c.Ncap + j] = s[m][n][e];
+          }
     }
     if (__any_sync(0xffffffffu, rise)) {
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          float top = fmaxf(in0 ? s[n][e] * f[2 * n + e] : -INFINITY, in1 ? s[n][e + 2] * f[2 * n + e] : -INFINITY);
+          const int i = 2 * n + e;
+          float top = -INFINITY;
+#pragma unroll
+          for (int m = 0; m < MT; ++m) top = fmaxf(top, fmaxf(s[m][n][e], s[m][n][e + 2]));
 #pragma unroll
           for (int o = 4; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-          const float m0 = mo[2 * n + e], a0 = ao[2 * n + e];
-          const float m1 = fmaxf(m0, top - kOff);
-          // F = exp2(m1 - a1) stays finite: a block of tiny values cannot lie more than 2^100 below
-          const float a1 = fmaxf(fmaxf(a0, top + lv - kOff), m1 - 100.f);
-          mo[2 * n + e] = m1;
-          ao[2 * n + e] = a1;
-          F[2 * n + e] = exp2f(m1 - a1);
-          l[2 * n + e] *= exp2f(m0 - m1);
-          const float r = exp2f(a0 - a1);
+          const float m0 = mo[i], a0 = ao[i];
+          const float m1 = top > m0 ? top + kSlack : m0;
+          // F vs stays below 2^100 and F below 2^112: blocks of tiny values lie at most 2^100 below
+          const float a1 = fmaxf(top + lv > a0 ? top + lv + kSlack : a0, fmaxf(m1 - 100.f, m1 + lv - 80.f));
+          mo[i] = m1;
+          ao[i] = a1;
+          F[i] = ex2(m1 - a1 + kSlack);
+          cv[i] = vs * F[i];
+          l[i] *= ex2(m0 - m1);
+          const float r = ex2(a0 - a1);
 #pragma unroll
-          for (int i = 0; i < D / 16; ++i) { acc[i][n][e] *= r; acc[i][n][e + 2] *= r; }
+          for (int k = 0; k < D / 16; ++k) { acc[k][n][e] *= r; acc[k][n][e + 2] *= r; }
         }
     }
     // ---- P, and O^T += V^T P^T
-    uint32_t p0[NT][2], p1[NT][2];
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      // kept finite: where it would overflow, every probability it meets is 0 (a NaN scale stays one)
-      float w[4], cv[2] = {vs * F[2 * n], vs * F[2 * n + 1]};
-      cv[0] = cv[0] > 3e38f ? 3e38f : cv[0];
-      cv[1] = cv[1] > 3e38f ? 3e38f : cv[1];
+    for (int m = 0; m < MT; ++m) {
+      uint32_t p0[NT][2], p1[NT][2];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        float x = exp2f(fmaf(s[n][e], f[2 * n + (e & 1)], -mo[2 * n + (e & 1)]));
-        if (!whole) x = (e < 2 ? in0 : in1) ? x : 0.f;
-        l[2 * n + (e & 1)] += x;
-        w[e] = x * cv[e & 1];
-      }
+      for (int n = 0; n < NT; ++n) {
+        float w[4];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const uint32_t hi = pack_f16(w[2 * i], w[2 * i + 1]);
-        p0[n][i] = transpose8(hi);
-        if (QT == 2) {
-          const float2 u = unpack_f16(hi);
-          p1[n][i] = transpose8(pack_f16(w[2 * i] - u.x, w[2 * i + 1] - u.y));
+        for (int e = 0; e < 4; ++e) {
+          const float x = ex2(s[m][n][e] - mo[2 * n + (e & 1)]);
+          l[2 * n + (e & 1)] += x;
+          w[e] = x * cv[2 * n + (e & 1)];
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint32_t hi = pack_f16(w[2 * i], w[2 * i + 1]);
+          p0[n][i] = transpose8(hi);
+          if (QT == 2) {
+            const float2 u = unpack_f16(hi);
+            p1[n][i] = transpose8(pack_f16(w[2 * i] - u.x, w[2 * i + 1] - u.y));
+          }
         }
       }
-    }
+      uint32_t vw[4][VW];
 #pragma unroll
-    for (int w = 0; w < VW; ++w) {
-      uint32_t u[4], v[4];
-      Wd::pairs(Wd::prep(vw[0][w]), Wd::prep(vw[1][w]), u);
-      Wd::pairs(Wd::prep(vw[2][w]), Wd::prep(vw[3][w]), v);
+      for (int i = 0; i < 4; ++i) read_row<8, D>(vw[i], vt, 16 * m + 2 * t + (i & 1) + 8 * (i >> 1), g);
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const uint32_t op[4] = {u[2 * e], u[2 * e + 1], v[2 * e], v[2 * e + 1]};
+      for (int w = 0; w < VW; ++w) {
+        uint32_t u[4], v[4];
+        Wd::pairs(Wd::prep(vw[0][w]), Wd::prep(vw[1][w]), u);
+        Wd::pairs(Wd::prep(vw[2][w]), Wd::prep(vw[3][w]), v);
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          mma_f16(acc[2 * w + e][n], op, p0[n][0], p0[n][1]);
-          if (QT == 2) mma_f16(acc[2 * w + e][n], op, p1[n][0], p1[n][1]);
+        for (int e = 0; e < 2; ++e) {
+          const uint32_t op[4] = {u[2 * e], u[2 * e + 1], v[2 * e], v[2 * e + 1]};
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            if (QT == 1) {
+              mma_f16(acc[2 * w + e][n], op, p0[n][0], p0[n][1]);
+            } else {
+              // a tile's products are summed apart: the product unit's sums are not rounded to nearest
+              float y[4] = {0.f, 0.f, 0.f, 0.f};
+              mma_f16(y, op, p1[n][0], p1[n][1]);
+              mma_f16(y, op, p0[n][0], p0[n][1]);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) acc[2 * w + e][n][i] += y[i];
+            }
+          }
         }
       }
     }
@@ -734,22 +820,21 @@ kv8_attn_kernel(const __grid_constant__ Kv8AttnArgs a) {
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const int i = 2 * n + e;
-      m[i] = mo[i] > kUnset ? mo[i] + kOff : -INFINITY;
+      m[i] = mo[i] > kUnset ? mo[i] : -INFINITY;
 #pragma unroll
       for (int o = 4; o < 32; o <<= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], o);
-      l[i] *= 0.0625f;                           // 2^-kOff
-      const float unit = 0.0625f / F[i];
+      const float unit = 1.f / F[i];
 #pragma unroll
       for (int k = 0; k < D / 16; ++k) { acc[k][n][e] *= unit; acc[k][n][e + 2] *= unit; }
     }
-  join_store<D, NT>(a, sm, at, acc, m, l, [&](int w) { return word_at<8>(D, w, g); });
+  join_store<D, NT, MT>(a, sm, at, acc, m, l, [&](int w) { return word_at<8>(D, w, g); });
 }
 
-template <int CODE, int D, int NT, int QT>
+template <int CODE, int D, int NT, int MT, int QT>
 cudaError_t launch_split(const Kv8AttnArgs& a, cudaStream_t st) {
   const lla_kv8_cache& c = a.p.cache;
-  constexpr size_t smem = sizeof(Smem<D, NT>);
-  auto* kern = kv8_attn_kernel<CODE, D, NT, QT>;
+  constexpr size_t smem = sizeof(Smem<D, NT, MT>);
+  auto* kern = kv8_attn_kernel<CODE, D, NT, MT, QT>;
   if (smem > 48 * 1024) {
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
@@ -757,12 +842,14 @@ cudaError_t launch_split(const Kv8AttnArgs& a, cudaStream_t st) {
   return launch_kernel(kern, dim3(a.ST, ceil_div(a.rows, 8 * NT) * c.H, c.B), dim3(AT), smem, st, 1, a);
 }
 
+// the planner chooses nt; a step of two tiles needs blocks of 32 tokens
 template <int CODE, int D, int QT>
 cudaError_t launch_rows(const Kv8AttnArgs& a, cudaStream_t st) {
-  if (a.nt == 1) return launch_split<CODE, D, 1, QT>(a, st);
-  if constexpr (D <= 128)
-    if (a.nt == 4) return launch_split<CODE, D, 4, QT>(a, st);
-  return launch_split<CODE, D, 2, QT>(a, st);
+  if (a.nt == 1) return launch_split<CODE, D, 1, 1, QT>(a, st);
+  if (a.p.cache.block < 32) return launch_split<CODE, D, 2, 1, QT>(a, st);
+  if constexpr (D <= 128 && QT == 1)
+    if (a.nt == 4) return launch_split<CODE, D, 4, 2, QT>(a, st);
+  return launch_split<CODE, D, 2, 2, QT>(a, st);
 }
 
 template <int CODE, int QT>
