@@ -18,6 +18,7 @@ Entry points (names as in the C ABI):
 """
 
 import ctypes
+import struct
 
 from . import _abi
 from ._abi import (LLA_BF16, LLA_ERR_CUDA, LLA_F32, LLA_FP8_E4M3, LLA_KV8_E4M3, LLA_KV8_I8,  # noqa: F401
@@ -409,74 +410,128 @@ def lla_decode_attn(*, workspace=None, stream=None, **kw):
 
 
 # -------------------------------------------------------- 8-bit K/V cache --
+# These are called once for each layer, loop and token, so they keep the host's
+# share small: each tensor's attributes are read once, and a call's parameters
+# are packed in one go.
+_CACHE_FMT = "6i2P2q2P2q"
+_I32_FMT = "Pi4x"
+
+
+def _packer(struct_type, fmt):
+    s = struct.Struct("@" + fmt)
+    if s.size != ctypes.sizeof(struct_type):
+        raise AssertionError(f"{struct_type.__name__}: {s.size} packed bytes, {ctypes.sizeof(struct_type)} expected")
+    return lambda *values: struct_type.from_buffer_copy(s.pack(*values))
+
+
+_pack_write = _packer(_abi.Kv8WriteParams, _CACHE_FMT + "2P3i4x3qi4x" + 3 * _I32_FMT)
+_pack_attn = _packer(_abi.Kv8AttnParams, _CACHE_FMT + _I32_FMT + "2i2Pi4x4q2P2i3q" + 2 * _I32_FMT + "f4xP2q")
+_pack_evict = _packer(_abi.Kv8EvictParams, 2 * _CACHE_FMT + "P2qP2q2P3i4xP")
+
+
 def _kv8_cache(k8, v8, k_scale, v_scale):
-    """[B,H,Ncap,d] codes and [B,H,Ncap/block] scales as the ABI's struct."""
+    """[B,H,Ncap,d] codes and [B,H,Ncap/block] scales as the values of the ABI's struct."""
     torch = _torch()
-    if k8.dtype == torch.int8:
+    dtype, shape, st, sshape, ss = k8.dtype, k8.shape, k8.stride(), k_scale.shape, k_scale.stride()
+    if dtype is torch.int8:
         code = LLA_KV8_I8
-    elif k8.dtype == torch.float8_e4m3fn:
+    elif dtype is torch.float8_e4m3fn:
         code = LLA_KV8_E4M3
     else:
-        raise TypeError(f"unsupported code dtype {k8.dtype}; use int8 or float8_e4m3fn")
-    if v8.dtype != k8.dtype or k_scale.dtype != torch.float32 or v_scale.dtype != torch.float32:
+        raise TypeError(f"unsupported code dtype {dtype}; use int8 or float8_e4m3fn")
+    if v8.dtype is not dtype or k_scale.dtype is not torch.float32 or v_scale.dtype is not torch.float32:
         raise TypeError("k8 and v8 share a dtype, scales are float32")
-    shape, sshape = k8.shape, k_scale.shape
-    if len(shape) != 4 or v8.shape != shape or v8.stride() != k8.stride():
+    if len(shape) != 4 or v8.shape != shape or v8.stride() != st:
         raise ValueError("k8 and v8 are [B,H,Ncap,d] with the same strides")
-    B, H, cap, d = shape
-    if (len(sshape) != 3 or v_scale.shape != sshape or v_scale.stride() != k_scale.stride() or sshape[0] != B
-            or sshape[1] != H or (cap % sshape[2] if sshape[2] else cap)):
+    if len(sshape) != 3 or v_scale.shape != sshape or v_scale.stride() != ss:
         raise ValueError("k_scale and v_scale are [B,H,Ncap/block] with the same strides")
-    _dense_inner(k8, 2, "k8")
-    _dense_inner(k_scale, 1, "k_scale")
-    st, ss = k8.stride(), k_scale.stride()
+    B, H, cap, d = shape
+    sB, sH, nb = sshape
+    if sB != B or sH != H or (cap % nb if nb else cap):
+        raise ValueError("k_scale and v_scale are [B,H,Ncap/block] of k8's B, H and Ncap")
+    sb, sh, sn, sd = st
+    if sd != 1 or (sn != d and cap > 1):
+        raise ValueError("k8 and v8: inner axes must be dense")
+    if ss[2] != 1 and nb > 1:
+        raise ValueError("k_scale and v_scale: inner axis must be dense")
     # an axis of one element may carry any stride
-    sh, ssh = (st[1] if H > 1 else cap * d), (ss[1] if H > 1 else sshape[2])
-    return _abi.Kv8Cache(B, H, d, cap // sshape[2] if sshape[2] else 16, cap, code, k8.data_ptr(), v8.data_ptr(),
-                         st[0] if B > 1 else H * sh, sh, k_scale.data_ptr(), v_scale.data_ptr(),
-                         ss[0] if B > 1 else H * ssh, ssh)
+    if H == 1:
+        sh = cap * d
+    if B == 1:
+        sb = H * sh
+    qh = ss[1] if H > 1 else nb
+    qb = ss[0] if B > 1 else H * qh
+    return (B, H, d, cap // nb if nb else 16, cap, code, k8.data_ptr(), v8.data_ptr(), sb, sh, k_scale.data_ptr(),
+            v_scale.data_ptr(), qb, qh)
 
 
 def _i32(v, B, name):
-    """An int for every sequence, or an int32 tensor [B]."""
-    if isinstance(v, _torch().Tensor):
-        if v.dtype != _torch().int32 or v.dim() != 1 or v.shape[0] != B or not v.is_contiguous():
+    """An int for every sequence, or an int32 tensor [B]: (address, value)."""
+    if v.__class__ is int:
+        return 0, v
+    torch = _torch()
+    if isinstance(v, torch.Tensor):
+        if v.dtype is not torch.int32 or v.shape != (B,) or (v.stride(0) != 1 and B > 1):
             raise ValueError(f"{name} is an int or a contiguous int32 tensor [B]")
-        return _abi.I32(v.data_ptr(), 0)
-    return _abi.I32(None, int(v))
+        return v.data_ptr(), 0
+    return 0, int(v)
 
 
-def _tensors(*ts):
-    return [t for t in ts if isinstance(t, _torch().Tensor)]
+def _kv8_device(*ts):
+    """The one CUDA device of the tensors among the arguments."""
+    Tensor, dev = _torch().Tensor, None
+    for t in ts:
+        if isinstance(t, Tensor):
+            i = t.get_device()
+            if i != dev:
+                if dev is not None or i < 0:
+                    _cuda(*[x for x in ts if isinstance(x, Tensor)])     # raises
+                dev = i
+    return dev
 
 
 def _rows16(t, what):
-    """Strides of the outer axes, those of one element replaced by 0."""
-    _dense_inner(t, 1, what)
-    return [s if n > 1 else 0 for n, s in zip(t.shape[:-1], t.stride()[:-1])]
+    """Strides of the outer axes of t [B,rows,H,d], those of one element replaced by 0."""
+    n0, n1, n2, d = t.shape
+    s0, s1, s2, s3 = t.stride()
+    if s3 != 1 and d > 1:
+        raise ValueError(f"{what}: the inner axis must be dense")
+    return s0 if n0 > 1 else 0, s1 if n1 > 1 else 0, s2 if n2 > 1 else 0
 
 
 def _on(dev, fn, where, params, *mid, stream):
-    """Call fn on dev's stream, with dev current."""
-    torch = _torch()
-    handle = _stream_handle(stream, dev)
-    if dev.index == torch.cuda.current_device():
-        st = fn(ctypes.byref(params), *mid, handle)
+    """Call fn on a stream of device number dev, with that device current."""
+    cuda = _torch().cuda
+    handle = (cuda.current_stream(dev) if stream is None else stream).cuda_stream
+    if dev == cuda.current_device():
+        st = fn(params, *mid, handle)
     else:
-        with torch.cuda.device(dev):
-            st = fn(ctypes.byref(params), *mid, handle)
+        with cuda.device(dev):
+            st = fn(params, *mid, handle)
     if st != 0:
         raise LLAError(st, where)
 
 
-def _kv8_workspace(nbytes, dev, workspace, stream):
-    if nbytes and workspace is None:
-        ws = _torch().empty(nbytes, dtype=_torch().uint8, device=dev)
+def _kv8_workspace(size, params, dev, workspace, stream):
+    """(address, bytes, tensor) of a call's scratch; sizes follow dev's processor count."""
+    cuda = _torch().cuda
+    if dev == cuda.current_device():
+        need = size(params)
+    else:
+        with cuda.device(dev):
+            need = size(params)
+    if need and workspace is None:
+        workspace = _torch().empty(need, dtype=_torch().uint8, device=f"cuda:{dev}")
         if stream is not None:
-            ws.record_stream(stream)     # its memory is not handed out again before the call has run
-        return ws.data_ptr(), nbytes, ws
-    ptr, nb = _workspace(nbytes, dev, workspace)
-    return ptr, nb, workspace
+            workspace.record_stream(stream)     # its memory is not handed out again before the call has run
+    elif need and workspace.get_device() != dev:
+        raise ValueError("workspace is on another device")
+    if not need:
+        return None, 0, None
+    have = workspace.numel() * workspace.element_size()
+    if have < need:
+        raise ValueError(f"workspace too small: {have} < {need} bytes")
+    return workspace.data_ptr(), have, workspace
 
 
 def lla_kv8_write(*, k, v, k8, v8, k_scale, v_scale, n=None, max_n=None, src0=0, row0=0, ring=False, stream=None):
@@ -489,68 +544,74 @@ def lla_kv8_write(*, k, v, k8, v8, k_scale, v_scale, n=None, max_n=None, src0=0,
     for all sequences or an int32 CUDA tensor [B]; n defaults to `rows`, and a
     tensor n needs max_n, its bound (default: the least of rows and Ncap).
     """
-    dev = _cuda(k, v, k8, v8, k_scale, v_scale, *_tensors(n, src0, row0))
+    dev = _kv8_device(k, v, k8, v8, k_scale, v_scale, n, src0, row0)
     c = _kv8_cache(k8, v8, k_scale, v_scale)
-    if k.dim() != 4 or k.shape != v.shape or k.stride() != v.stride() or k.dtype != v.dtype:
+    B, shape = c[0], k.shape
+    if len(shape) != 4 or v.shape != shape or k.stride() != v.stride() or k.dtype is not v.dtype:
         raise ValueError("k and v are [B,rows,H,d] and match in shape, strides and dtype")
-    if k.shape[0] != c.B or k.shape[2] != c.H or k.shape[3] != c.d:
+    rows = shape[1]
+    if shape[0] != B or shape[2] != c[1] or shape[3] != c[2]:
         raise ValueError("k and v are [B,rows,H,d] of the cache's B, H and d")
-    rows = k.shape[1]
-    n = rows if n is None else n
+    if n is None:
+        n = rows
     if max_n is None:
-        max_n = n if isinstance(n, int) else min(rows, c.Ncap)
-    sb, sn, sh = _rows16(k, "k")
-    p = _abi.Kv8WriteParams(c, k.data_ptr(), v.data_ptr(), _dtype_code(k), rows, int(bool(ring)), sb, sn, sh,
-                            int(max_n), _i32(n, c.B, "n"), _i32(src0, c.B, "src0"), _i32(row0, c.B, "row0"))
+        max_n = n if isinstance(n, int) else min(rows, c[4])
+    p = _pack_write(*c, k.data_ptr(), v.data_ptr(), _dtype_code(k), rows, 1 if ring else 0, *_rows16(k, "k and v"),
+                    max_n, *_i32(n, B, "n"), *_i32(src0, B, "src0"), *_i32(row0, B, "row0"))
     _on(dev, lib().lla_kv8_write, "lla_kv8_write", p, stream=stream)
 
 
 def _kv8_attn_params(q, k8, v8, k_scale, v_scale, lens, out, win_k=None, win_v=None, ctx=None, tail=0, scale=0.0,
                      weights=None):
     c = _kv8_cache(k8, v8, k_scale, v_scale)
-    if q.dim() != 4 or q.shape[0] != c.B or q.shape[3] != c.d or q.shape[2] % c.H or q.shape[2] == 0:
+    B, H, d = c[:3]
+    shape = q.shape
+    if len(shape) != 4 or shape[0] != B or shape[3] != d or shape[2] % H or shape[2] == 0:
         raise ValueError("q is [B,nq,H*G,d] of the cache's B, H and d")
-    if out.shape != q.shape or out.dtype != q.dtype:
+    if out.shape != shape or out.dtype is not q.dtype:
         raise ValueError("out must have q's shape and dtype")
-    nq = q.shape[1]
-    _dense_inner(q, 2, "q")
-    _dense_inner(out, 2, "out")
-    qs, os_ = q.stride(), out.stride()
-    row = q.shape[2] * c.d
-    p = _abi.Kv8AttnParams(c, _i32(lens, c.B, "lens"), nq, q.shape[2] // c.H, q.data_ptr(), out.data_ptr(),
-                           _dtype_code(q), qs[0] if c.B > 1 else 0, qs[1] if nq > 1 else 0,
-                           os_[0] if c.B > 1 else nq * row, os_[1] if nq > 1 else row)
+    _, nq, heads, _ = shape
+    row = heads * d
+    qb, qn, qh, qd = q.stride()
+    ob, on, oh, od = out.stride()
+    if qd != 1 or od != 1 or (heads > 1 and (qh != d or oh != d)):
+        raise ValueError("q and out: inner axes must be dense")
+    win = (0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0)
     if win_k is not None:
-        if (win_v is None or win_k.dim() != 4 or win_k.shape != win_v.shape or win_k.stride() != win_v.stride()
-                or win_k.dtype != win_v.dtype):
+        ws = win_k.shape
+        if (win_v is None or len(ws) != 4 or win_v.shape != ws or win_k.stride() != win_v.stride()
+                or win_k.dtype is not win_v.dtype):
             raise ValueError("win_k and win_v are [B,Wcap,H,d] and match in shape, strides and dtype")
-        if win_k.shape[0] != c.B or win_k.shape[2] != c.H or win_k.shape[3] != c.d:
+        if ws[0] != B or ws[2] != H or ws[3] != d:
             raise ValueError("win_k and win_v are [B,Wcap,H,d] of the cache's B, H and d")
         if ctx is None:
             raise ValueError("win_k needs ctx, the context length")
-        p.win_k, p.win_v, p.win_dtype, p.Wcap = win_k.data_ptr(), win_v.data_ptr(), _dtype_code(win_k), win_k.shape[1]
-        p.win_stride_b, p.win_stride_n, p.win_stride_h = _rows16(win_k, "win_k")
-        p.ctx, p.tail = _i32(ctx, c.B, "ctx"), _i32(tail, c.B, "tail")
+        win = (win_k.data_ptr(), win_v.data_ptr(), _dtype_code(win_k), ws[1], *_rows16(win_k, "win_k and win_v"),
+               *_i32(ctx, B, "ctx"), *_i32(tail, B, "tail"))
     elif win_v is not None:
         raise ValueError("win_v without win_k")
-    p.scale = scale
-    if weights is not None:
-        p.weights, p.weights_stride_b, p.weights_stride_h = _kv8_weights(weights, c)
-    return p
+    w = (0, 0, 0) if weights is None else _kv8_weights(weights, c)
+    return _pack_attn(*c, *_i32(lens, B, "lens"), nq, heads // H, q.data_ptr(), out.data_ptr(), _dtype_code(q),
+                      qb if B > 1 else 0, qn if nq > 1 else 0, ob if B > 1 else nq * row, on if nq > 1 else row,
+                      *win, scale, *w)
 
 
 def _kv8_weights(w, c):
-    if w.dtype != _torch().float32 or tuple(w.shape) != (c.B, c.H, c.Ncap):
+    B, H, cap = c[0], c[1], c[4]
+    if w.dtype is not _torch().float32 or w.shape != (B, H, cap):
         raise ValueError("weights are float32 [B,H,Ncap]")
-    _dense_inner(w, 1, "weights")
-    sh = w.stride(1) if c.H > 1 else c.Ncap
-    return w.data_ptr(), w.stride(0) if c.B > 1 else c.H * sh, sh
+    sb, sh, sn = w.stride()
+    if sn != 1 and cap > 1:
+        raise ValueError("weights: the inner axis must be dense")
+    if H == 1:
+        sh = cap
+    return w.data_ptr(), sb if B > 1 else H * sh, sh
 
 
 def lla_kv8_attn_workspace_bytes(**kw):
     kw.pop("workspace", None)
     kw.pop("stream", None)
-    return lib().lla_kv8_attn_workspace_bytes(ctypes.byref(_kv8_attn_params(**kw)))
+    return lib().lla_kv8_attn_workspace_bytes(_kv8_attn_params(**kw))
 
 
 def lla_kv8_attn(*, q, k8, v8, k_scale, v_scale, lens, out, win_k=None, win_v=None, ctx=None, tail=0, scale=0.0,
@@ -566,32 +627,36 @@ def lla_kv8_attn(*, q, k8, v8, k_scale, v_scale, lens, out, win_k=None, win_v=No
     [B,H,Ncap] float32, optional: the softmax weights of the cached tokens are
     added, summed over the queries of their head.  scale 0: 1/sqrt(d).
     """
-    dev = _cuda(q, k8, v8, k_scale, v_scale, out, win_k, win_v, weights, *_tensors(lens, ctx, tail))
+    dev = _kv8_device(q, k8, v8, k_scale, v_scale, out, win_k, win_v, weights, lens, ctx, tail)
     p = _kv8_attn_params(q, k8, v8, k_scale, v_scale, lens, out, win_k, win_v, ctx, tail, scale, weights)
     L = lib()
-    ws, nb, _keep = _kv8_workspace(L.lla_kv8_attn_workspace_bytes(ctypes.byref(p)), dev, workspace, stream)
+    ws, nb, _keep = _kv8_workspace(L.lla_kv8_attn_workspace_bytes, p, dev, workspace, stream)
     _on(dev, L.lla_kv8_attn, "lla_kv8_attn", p, ws, nb, stream=stream)
 
 
 def _kv8_evict_params(k8, v8, k_scale, v_scale, weights, lens, keep, first=0, last=1, to=None, kept=None):
+    torch = _torch()
     c = _kv8_cache(k8, v8, k_scale, v_scale)
+    w = _kv8_weights(weights, c)
     if to is None:
-        to = dict(k8=k8, v8=v8, k_scale=k_scale, v_scale=v_scale, weights=weights, lens=lens)
-    t = _kv8_cache(to["k8"], to["v8"], to["k_scale"], to["v_scale"])
-    for x, nm in ((lens, "lens"), (to["lens"], "to['lens']")):
-        if x.dtype != _torch().int32 or tuple(x.shape) != (c.B,) or not x.is_contiguous():
-            raise ValueError(f"{nm} is a contiguous int32 tensor [B]")
-    if kept is not None and (kept.dtype != _torch().int32 or tuple(kept.shape) != (c.B, c.H, keep)
+        t, tw, to_lens = c, w, lens
+    else:
+        t = _kv8_cache(to["k8"], to["v8"], to["k_scale"], to["v_scale"])
+        tw, to_lens = _kv8_weights(to["weights"], t), to["lens"]
+    for x in (lens, to_lens):
+        if x.dtype is not torch.int32 or x.shape != (c[0],) or not x.is_contiguous():
+            raise ValueError("lens (and to['lens']) are contiguous int32 tensors [B]")
+    if kept is not None and (kept.dtype is not torch.int32 or kept.shape != (c[0], c[1], keep)
                              or not kept.is_contiguous()):
         raise ValueError("kept is a contiguous int32 tensor [B,H,keep]")
-    return _abi.Kv8EvictParams(c, t, *_kv8_weights(weights, c), *_kv8_weights(to["weights"], t), lens.data_ptr(),
-                               to["lens"].data_ptr(), keep, first, last, None if kept is None else kept.data_ptr())
+    return _pack_evict(*c, *t, *w, *tw, lens.data_ptr(), to_lens.data_ptr(), keep, first, last,
+                       0 if kept is None else kept.data_ptr())
 
 
 def lla_kv8_evict_workspace_bytes(**kw):
     kw.pop("workspace", None)
     kw.pop("stream", None)
-    return lib().lla_kv8_evict_workspace_bytes(ctypes.byref(_kv8_evict_params(**kw)))
+    return lib().lla_kv8_evict_workspace_bytes(_kv8_evict_params(**kw))
 
 
 def lla_kv8_evict(*, k8, v8, k_scale, v_scale, weights, lens, keep, first=0, last=1, to=None, kept=None,
@@ -606,8 +671,8 @@ def lla_kv8_evict(*, k8, v8, k_scale, v_scale, weights, lens, keep, first=0, las
     another Ncap).  kept [B,H,keep] int32, optional: source block of each block
     that stays, -1 where there is none.
     """
-    dev = _cuda(k8, v8, k_scale, v_scale, weights, lens, kept, *(to or {}).values())
+    dev = _kv8_device(k8, v8, k_scale, v_scale, weights, lens, kept, *(to.values() if to else ()))
     p = _kv8_evict_params(k8, v8, k_scale, v_scale, weights, lens, keep, first, last, to, kept)
     L = lib()
-    ws, nb, _keep = _kv8_workspace(L.lla_kv8_evict_workspace_bytes(ctypes.byref(p)), dev, workspace, stream)
+    ws, nb, _keep = _kv8_workspace(L.lla_kv8_evict_workspace_bytes, p, dev, workspace, stream)
     _on(dev, L.lla_kv8_evict, "lla_kv8_evict", p, ws, nb, stream=stream)

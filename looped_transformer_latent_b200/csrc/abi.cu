@@ -434,7 +434,8 @@ Kv8AttnPlan plan_kv8_attn(const lla_kv8_attn_params& p) {
     const int64_t ctas = bh * tiles, sms = num_sms(), per_sm = kv8_ctas_per_sm(c.d, pl.nt, f32 ? 2 : 1);
     const int64_t extra = 48 + 24 * pl.nt;       // tokens' worth of queries, join and partial results
     int64_t best = INT64_MAX;
-    for (int S = 1; S <= ceil_div(most, 128) && S <= 512; ++S) {
+    for (int S = 1, step = 1; S <= ceil_div(most, 128) && S <= 512; S += step) {
+      if (S == 4 * step) step *= 2;              // 1, 2, 3, 4, 6, 8, 12, 16, ...
       const int tps = (most + S - 1) / S + 127 & ~127;
       const int64_t n = ctas * ceil_div(most, tps);
       const int64_t shared = 2 * ((n + sms - 1) / sms), alone = per_sm * ((n + sms * per_sm - 1) / (sms * per_sm));

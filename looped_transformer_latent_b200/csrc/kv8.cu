@@ -7,23 +7,113 @@
 namespace lla {
 namespace {
 
-constexpr int WT = 128;          // threads of the writer
-
-// Largest magnitude as ordered bits: a NaN is above infinity, which is above
-// every finite value.
-__device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7fffffffu; }
 constexpr uint32_t kInfBits = 0x7f800000u;
 
-__device__ __forceinline__ uint8_t quantise(float x, float s, int code) {
-  const float y = x / s;         // fp32 quotient: the codes are a function of x and s alone
-  if (code == LLA_KV8_I8) return (uint8_t)(int8_t)fminf(fmaxf(rintf(y), -127.f), 127.f);
-  const __nv_fp8_e4m3 c(y);      // nearest-even, saturating to +-448
-  return *reinterpret_cast<const uint8_t*>(&c);
+// 8 consecutive elements as they come: bf16 in one 16-byte word, fp32 in two.
+template <int DT>
+struct Vec;
+template <>
+struct Vec<LLA_BF16> {
+  uint4 v;
+  __device__ __forceinline__ void load(const void* x, int64_t at) {
+    v = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(x) + at));
+  }
+  __device__ __forceinline__ void zero() { v = make_uint4(0, 0, 0, 0); }
+  // magnitude bits of the largest element, in fp32's places: NaN above infinity above every number
+  __device__ __forceinline__ uint32_t top() const {
+    const uint32_t m = 0x7fff7fffu;
+    const uint32_t a = __vmaxu2(__vmaxu2(v.x & m, v.y & m), __vmaxu2(v.z & m, v.w & m));
+    return max(a << 16, a & 0xffff0000u);
+  }
+  __device__ __forceinline__ void get(float (&f)[8]) const {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[2 * i] = __uint_as_float(w[i] << 16);
+      f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  }
+};
+template <>
+struct Vec<LLA_F32> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const void* x, int64_t at) {
+    const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(x) + at);
+    a = __ldg(p);
+    b = __ldg(p + 1);
+  }
+  __device__ __forceinline__ void zero() { a = b = make_float4(0, 0, 0, 0); }
+  __device__ __forceinline__ uint32_t top() const {
+    float f[8];
+    get(f);
+    uint32_t t = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) t = max(t, __float_as_uint(f[i]) & 0x7fffffffu);
+    return t;
+  }
+  __device__ __forceinline__ void get(float (&f)[8]) const {
+    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
+    f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+  }
+};
+
+__device__ __forceinline__ uint32_t e4m3_pair(float lo, float hi) {
+  return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);   // nearest-even, +-448
+}
+__device__ __forceinline__ uint32_t bytes4(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
 }
 
-// One CTA quantises one block of one head of one part: amax over its tokens,
-// then the codes.
-__global__ void __launch_bounds__(WT) kv8_write_kernel(const lla_kv8_write_params p) {
+// The codes of 8 elements: fp32 quotients x / s, rounded to nearest-even.  The
+// quotient and x * (1 / s) are off by 2^-24 and 2 x 2^-24 relative, so they round to
+// the same code unless they lie that near to a boundary between two; only then
+// is the division done (it is about ten instructions an element).  `fast`: 1 / s
+// is an ordinary number.
+template <int CODE>
+__device__ __forceinline__ uint2 quantise8(const float (&x)[8], float s, float inv, bool fast) {
+  bool sure = fast;
+  uint2 r;
+  if constexpr (CODE == LLA_KV8_I8) {
+    uint32_t c[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float t = fmaf(x[i], inv, 12582912.f);         // 1.5 x 2^23: the integer in the low bits
+      const float off = fmaf(x[i], inv, 12582912.f - t);   // exact to 2^-25
+      c[i] = __float_as_uint(t);
+      sure = sure && fabsf(off) < 0.49998f;                // |x / s| <= 127: both are off by 127 x 2^-24 = 7.6e-6 at most
+    }
+    r.x = bytes4(c[0], c[1], c[2], c[3]);
+    r.y = bytes4(c[4], c[5], c[6], c[7]);
+  } else {
+    // a little below and a little above the quotient: 2^-21 covers 3 x 2^-24 and the products' own rounding
+    const float lo = inv * (1.f - 0x1p-21f), hi = inv * (1.f + 0x1p-21f);
+    uint32_t a[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      a[i] = e4m3_pair(x[2 * i] * lo, x[2 * i + 1] * lo);
+      sure = sure && a[i] == e4m3_pair(x[2 * i] * hi, x[2 * i + 1] * hi);
+    }
+    r.x = a[0] | a[1] << 16;
+    r.y = a[2] | a[3] << 16;
+  }
+  if (!sure) {
+    uint32_t c[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float q = x[i] / s;
+      c[i] = CODE == LLA_KV8_I8 ? (uint32_t)(int)fminf(fmaxf(rintf(q), -127.f), 127.f) : e4m3_pair(q, 0.f);
+    }
+    r.x = bytes4(c[0], c[1], c[2], c[3]);
+    r.y = bytes4(c[4], c[5], c[6], c[7]);
+  }
+  return r;
+}
+
+// One CTA quantises one block of one head of one part.  NV vectors of 8 elements
+// a thread stay in registers between the maximum and the codes, so each element
+// is read once; NV = 0 reads them again (blocks of more than 16K elements).
+template <int CODE, int DT, int T, int NV>
+__global__ void __launch_bounds__(T) kv8_write_kernel(const lla_kv8_write_params p) {
   griddep_wait();
   const lla_kv8_cache& c = p.cache;
   const int h = blockIdx.y, b = blockIdx.z >> 1, part = blockIdx.z & 1;
@@ -33,31 +123,83 @@ __global__ void __launch_bounds__(WT) kv8_write_kernel(const lla_kv8_write_param
   const bool fits = row0 >= 0 && row0 % c.block == 0 && row0 + n <= c.Ncap &&
                     (p.ring ? n <= p.rows : src0 >= 0 && src0 + n <= p.rows);
   if (t0 >= n || !fits) return;
-  const int m = min(c.block, n - t0);
+  const int vpr = c.d / 8, nv = min(c.block, n - t0) * vpr;   // vectors of a row, of the block
   const void* x = part ? p.x_v : p.x_k;
   const int64_t xb = (int64_t)b * p.x_stride_b + (int64_t)h * p.x_stride_h;
-  auto src = [&](int j) -> int64_t {
-    int64_t r = src0 + t0 + j;
-    if (p.ring) { r %= p.rows; if (r < 0) r += p.rows; }
-    return xb + r * p.x_stride_n;
+  int64_t first = src0 + t0;                               // source row of the block's first token
+  if (p.ring) { first %= p.rows; if (first < 0) first += p.rows; }
+  const int row_step = T / vpr, col_step = T % vpr;
+  int row = threadIdx.x / vpr, col = threadIdx.x % vpr;
+  auto next = [&]() -> int64_t {                           // element offset of the thread's next vector
+    int64_t r = first + row;
+    if (p.ring && r >= p.rows) r -= p.rows;                // n <= rows: at most one turn
+    const int64_t at = xb + r * p.x_stride_n + 8 * col;
+    row += row_step; col += col_step;
+    if (col >= vpr) { col -= vpr; ++row; }
+    return at;
   };
+  constexpr int HOLD = NV ? NV : 1;
+  Vec<DT> v[HOLD];
   uint32_t top = 0;
-  for (int e = threadIdx.x; e < m * c.d; e += WT)
-    top = max(top, abs_bits(load_elem(x, src(e / c.d) + e % c.d, p.dtype)));
-  __shared__ uint32_t tops[WT / 32];
+  if constexpr (NV > 0) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int64_t at = next();
+      if ((int)threadIdx.x + i * T < nv) v[i].load(x, at);
+      else v[i].zero();
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) top = max(top, v[i].top());
+  } else {
+    for (int i = threadIdx.x; i < nv; i += T) {
+      v[0].load(x, next());
+      top = max(top, v[0].top());
+    }
+  }
+  __shared__ uint32_t tops[T / 32];
   top = __reduce_max_sync(0xffffffffu, top);
   if (threadIdx.x % 32 == 0) tops[threadIdx.x / 32] = top;
   __syncthreads();
-  for (int w = 0; w < WT / 32; ++w) top = max(top, tops[w]);
+#pragma unroll
+  for (int w = 0; w < T / 32; ++w) top = max(top, tops[w]);
   const bool bad = top >= kInfBits;
-  const float s = bad ? __int_as_float(0x7fc00000) : __uint_as_float(top) / (c.code == LLA_KV8_I8 ? 127.f : 448.f);
+  const float s = bad ? __int_as_float(0x7fc00000) : __uint_as_float(top) / (CODE == LLA_KV8_I8 ? 127.f : 448.f);
+  const float inv = 1.f / s;
+  const bool some = s > 0.f, fast = s > 1e-37f;
   uint8_t* out = static_cast<uint8_t*>(part ? c.v : c.k) + (int64_t)b * c.stride_b + (int64_t)h * c.stride_h +
                  (row0 + t0) * c.d;
-  for (int e = threadIdx.x; e < m * c.d; e += WT)
-    out[e] = s > 0.f ? quantise(load_elem(x, src(e / c.d) + e % c.d, p.dtype), s, c.code) : 0;
+  auto put = [&](int i, const Vec<DT>& y) {
+    float f[8];
+    y.get(f);
+    const uint2 r = some ? quantise8<CODE>(f, s, inv, fast) : make_uint2(0, 0);
+    *reinterpret_cast<uint2*>(out + 8 * (int64_t)i) = r;
+  };
+  if constexpr (NV > 0) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      if ((int)threadIdx.x + i * T < nv) put(threadIdx.x + i * T, v[i]);
+  } else {
+    row = threadIdx.x / vpr; col = threadIdx.x % vpr;
+    for (int i = threadIdx.x; i < nv; i += T) {
+      v[0].load(x, next());
+      put(i, v[0]);
+    }
+  }
   if (threadIdx.x == 0)
     (part ? c.v_scale : c.k_scale)[(int64_t)b * c.scale_stride_b + (int64_t)h * c.scale_stride_h +
                                    (row0 + t0) / c.block] = s;
+}
+
+template <int CODE, int DT>
+cudaError_t launch_write(const lla_kv8_write_params& p, cudaStream_t st) {
+  const dim3 grid(ceil_div(p.max_n, p.cache.block), p.cache.H, 2 * p.cache.B);
+  const int nv = p.cache.block * p.cache.d / 8;
+  if (nv <= 128) return launch_kernel(kv8_write_kernel<CODE, DT, 128, 1>, grid, dim3(128), 0, st, 1, p);
+  if (nv <= 256) return launch_kernel(kv8_write_kernel<CODE, DT, 128, 2>, grid, dim3(128), 0, st, 1, p);
+  if (nv <= 512) return launch_kernel(kv8_write_kernel<CODE, DT, 128, 4>, grid, dim3(128), 0, st, 1, p);
+  if (nv <= 1024) return launch_kernel(kv8_write_kernel<CODE, DT, 256, 4>, grid, dim3(256), 0, st, 1, p);
+  if (nv <= 2048) return launch_kernel(kv8_write_kernel<CODE, DT, 256, 8>, grid, dim3(256), 0, st, 1, p);
+  return launch_kernel(kv8_write_kernel<CODE, DT, 256, 0>, grid, dim3(256), 0, st, 1, p);
 }
 
 // ---------------------------------------------------------------- eviction --
@@ -227,8 +369,9 @@ __global__ void __launch_bounds__(MT) kv8_move_kernel(const Kv8EvictArgs a, int 
 }  // namespace
 
 cudaError_t launch_kv8_write(const lla_kv8_write_params& p, cudaStream_t st) {
-  const dim3 grid(ceil_div(p.max_n, p.cache.block), p.cache.H, 2 * p.cache.B);
-  return launch_kernel(kv8_write_kernel, grid, dim3(WT), 0, st, 1, p);
+  if (p.cache.code == LLA_KV8_I8)
+    return p.dtype == LLA_BF16 ? launch_write<LLA_KV8_I8, LLA_BF16>(p, st) : launch_write<LLA_KV8_I8, LLA_F32>(p, st);
+  return p.dtype == LLA_BF16 ? launch_write<LLA_KV8_E4M3, LLA_BF16>(p, st) : launch_write<LLA_KV8_E4M3, LLA_F32>(p, st);
 }
 
 cudaError_t launch_kv8_evict(const Kv8EvictArgs& a, cudaStream_t st) {

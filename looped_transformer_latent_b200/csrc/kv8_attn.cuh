@@ -835,8 +835,9 @@ cudaError_t launch_split(const Kv8AttnArgs& a, cudaStream_t st) {
   const lla_kv8_cache& c = a.p.cache;
   constexpr size_t smem = sizeof(Smem<D, NT, MT>);
   auto* kern = kv8_attn_kernel<CODE, D, NT, MT, QT>;
+  static std::atomic<uint64_t> done{0};
   if (smem > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    const cudaError_t e = allow_smem(kern, smem, done);
     if (e != cudaSuccess) return e;
   }
   return launch_kernel(kern, dim3(a.ST, ceil_div(a.rows, 8 * NT) * c.H, c.B), dim3(AT), smem, st, 1, a);
