@@ -2,6 +2,8 @@
 // of tokens and head.
 #include <cuda_fp8.h>
 
+#include <climits>
+
 #include "kernels.cuh"
 
 namespace lla {
@@ -118,24 +120,32 @@ __global__ void __launch_bounds__(T) kv8_write_kernel(const lla_kv8_write_params
   const lla_kv8_cache& c = p.cache;
   const int h = blockIdx.y, b = blockIdx.z >> 1, part = blockIdx.z & 1;
   const int n = min(max(kv8_at(p.n, b), 0), p.max_n);
-  const int t0 = blockIdx.x * c.block;
-  const int64_t src0 = kv8_at(p.src0, b), row0 = kv8_at(p.row0, b);
-  const bool fits = row0 >= 0 && row0 % c.block == 0 && row0 + n <= c.Ncap &&
-                    (p.ring ? n <= p.rows : src0 >= 0 && src0 + n <= p.rows);
-  if (t0 >= n || !fits) return;
-  const int vpr = c.d / 8, nv = min(c.block, n - t0) * vpr;   // vectors of a row, of the block
+  const int bshift = 31 - __clz(c.block), t0 = blockIdx.x << bshift;
+  if (t0 >= n) return;
+  const int src0 = kv8_at(p.src0, b), row0 = kv8_at(p.row0, b);
+  // n <= Ncap and n <= rows: the differences do not overflow
+  const bool fits = row0 >= 0 && (row0 & (c.block - 1)) == 0 && row0 <= c.Ncap - n &&
+                    (p.ring ? n <= p.rows : src0 >= 0 && src0 <= p.rows - n);
+  if (!fits) return;
+  const uint32_t vpr = c.d >> 3;                           // vectors of a row
+  const int nv = min(c.block, n - t0) * vpr;               // and of the block
   const void* x = part ? p.x_v : p.x_k;
-  const int64_t xb = (int64_t)b * p.x_stride_b + (int64_t)h * p.x_stride_h;
-  int64_t first = src0 + t0;                               // source row of the block's first token
-  if (p.ring) { first %= p.rows; if (first < 0) first += p.rows; }
+  int first = src0 + t0;                                   // source row of the block's first token
+  if (p.ring) {
+    first = src0 % p.rows;
+    if (first < 0) first += p.rows;
+    first = (int)(((uint32_t)first + (uint32_t)t0) % (uint32_t)p.rows);
+  }
+  // threads run through the rows of the block; a ring's rows turn once at most (n <= rows)
+  const int64_t xb = (int64_t)b * p.x_stride_b + (int64_t)h * p.x_stride_h + first * p.x_stride_n;
+  const int64_t turn = p.ring ? (int64_t)p.rows * p.x_stride_n : 0;
+  const int turn_row = p.ring ? p.rows - first : INT_MAX;
   const int row_step = T / vpr, col_step = T % vpr;
   int row = threadIdx.x / vpr, col = threadIdx.x % vpr;
   auto next = [&]() -> int64_t {                           // element offset of the thread's next vector
-    int64_t r = first + row;
-    if (p.ring && r >= p.rows) r -= p.rows;                // n <= rows: at most one turn
-    const int64_t at = xb + r * p.x_stride_n + 8 * col;
+    const int64_t at = xb + row * p.x_stride_n + 8 * col - (row >= turn_row ? turn : 0);
     row += row_step; col += col_step;
-    if (col >= vpr) { col -= vpr; ++row; }
+    if (col >= (int)vpr) { col -= vpr; ++row; }
     return at;
   };
   constexpr int HOLD = NV ? NV : 1;
@@ -167,7 +177,7 @@ __global__ void __launch_bounds__(T) kv8_write_kernel(const lla_kv8_write_params
   const float inv = 1.f / s;
   const bool some = s > 0.f, fast = s > 1e-37f;
   uint8_t* out = static_cast<uint8_t*>(part ? c.v : c.k) + (int64_t)b * c.stride_b + (int64_t)h * c.stride_h +
-                 (row0 + t0) * c.d;
+                 (int64_t)(row0 + t0) * c.d;
   auto put = [&](int i, const Vec<DT>& y) {
     float f[8];
     y.get(f);
@@ -187,7 +197,7 @@ __global__ void __launch_bounds__(T) kv8_write_kernel(const lla_kv8_write_params
   }
   if (threadIdx.x == 0)
     (part ? c.v_scale : c.k_scale)[(int64_t)b * c.scale_stride_b + (int64_t)h * c.scale_stride_h +
-                                   (row0 + t0) / c.block] = s;
+                                   ((row0 + t0) >> bshift)] = s;
 }
 
 template <int CODE, int DT>
@@ -197,7 +207,11 @@ cudaError_t launch_write(const lla_kv8_write_params& p, cudaStream_t st) {
   if (nv <= 128) return launch_kernel(kv8_write_kernel<CODE, DT, 128, 1>, grid, dim3(128), 0, st, 1, p);
   if (nv <= 256) return launch_kernel(kv8_write_kernel<CODE, DT, 128, 2>, grid, dim3(128), 0, st, 1, p);
   if (nv <= 512) return launch_kernel(kv8_write_kernel<CODE, DT, 128, 4>, grid, dim3(128), 0, st, 1, p);
-  if (nv <= 1024) return launch_kernel(kv8_write_kernel<CODE, DT, 256, 4>, grid, dim3(256), 0, st, 1, p);
+  if constexpr (DT == LLA_BF16) {
+    if (nv <= 1024) return launch_kernel(kv8_write_kernel<CODE, DT, 128, 8>, grid, dim3(128), 0, st, 1, p);
+  } else {
+    if (nv <= 1024) return launch_kernel(kv8_write_kernel<CODE, DT, 256, 4>, grid, dim3(256), 0, st, 1, p);
+  }
   if (nv <= 2048) return launch_kernel(kv8_write_kernel<CODE, DT, 256, 8>, grid, dim3(256), 0, st, 1, p);
   return launch_kernel(kv8_write_kernel<CODE, DT, 256, 0>, grid, dim3(256), 0, st, 1, p);
 }
