@@ -684,12 +684,20 @@ kv8_attn_kernel(const __grid_constant__ Kv8AttnArgs a) {
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
           const uint2 q0 = sm.q[0][w][n][lane];
+          if (QT == 1) {
 #pragma unroll
-          for (int m = 0; m < MT; ++m) mma_f16(s[m][n], op[m], q0.x, q0.y);
-          if (QT == 2) {
+            for (int m = 0; m < MT; ++m) mma_f16(s[m][n], op[m], q0.x, q0.y);
+          } else {
+            // 16 elements' products are summed apart: the product unit's sums are not rounded to nearest
             const uint2 q1 = sm.q[1][w][n][lane];
 #pragma unroll
-            for (int m = 0; m < MT; ++m) mma_f16(s[m][n], op[m], q1.x, q1.y);
+            for (int m = 0; m < MT; ++m) {
+              float y[4] = {0.f, 0.f, 0.f, 0.f};
+              mma_f16(y, op[m], q1.x, q1.y);
+              mma_f16(y, op[m], q0.x, q0.y);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) s[m][n][e] += y[e];
+            }
           }
         }
       }
@@ -799,7 +807,7 @@ kv8_attn_kernel(const __grid_constant__ Kv8AttnArgs a) {
             if (QT == 1) {
               mma_f16(acc[2 * w + e][n], op, p0[n][0], p0[n][1]);
             } else {
-              // a tile's products are summed apart: the product unit's sums are not rounded to nearest
+              // as above
               float y[4] = {0.f, 0.f, 0.f, 0.f};
               mma_f16(y, op, p1[n][0], p1[n][1]);
               mma_f16(y, op, p0[n][0], p0[n][1]);
