@@ -18,7 +18,7 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "liblla.so")
 
 SOURCES = ["abi.cu", "writer.cu", "decode_simt.cu", "decode_tc.cu", "decode_fp8.cu", "maps.cu", "gemm_tc.cu",
-           "recon_tc.cu", "noalloc.cu", "kv8.cu", "kv8_attn.cu",
+           "recon_tc.cu", "noalloc.cu", "kv8.cu", "kv8_attn.cu", "kv8_wide.cu",
            "kv8_attn_i8_bf16.cu", "kv8_attn_i8_f32.cu", "kv8_attn_e4m3_bf16.cu", "kv8_attn_e4m3_f32.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 

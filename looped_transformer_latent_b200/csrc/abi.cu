@@ -402,7 +402,7 @@ int check_kv8_attn(const lla_kv8_attn_params& p) {
 }
 
 struct Kv8AttnPlan {
-  int rows_pass, nt, S, tps, ST, tpc;
+  int rows_pass, nt, wide, S, tps, ST, tpc;
   size_t o_ml, o_y, o_scores, bytes;
 };
 
@@ -427,12 +427,15 @@ Kv8AttnPlan plan_kv8_attn(const lla_kv8_attn_params& p) {
   // 32 rows of more than 128 elements, or with two terms of each, do not fit a thread's registers
   const bool f32 = p.dtype == LLA_F32;
   pl.nt = pl.rows_pass <= 8 ? 1 : pl.rows_pass <= 16 || c.d > 128 || c.block < 32 || f32 ? 2 : 4;
-  const int tiles = ceil_div(pl.rows_pass, 8 * pl.nt);
+  // 33 rows and more (bf16, d <= 128): the tcgen05 kernel.  256 heads of 128, 4096 e4m3 tokens: 48 rows 143 us there
+  // and 179 in the mma.sync kernel, 128 rows 198 and 302; 32 rows 127 and 123, int8 heads of 96 125 and 119.
+  pl.wide = f32 || c.d > 128 || pl.rows_pass <= 32 ? 0 : pl.rows_pass <= 64 ? 64 : 128;
+  const int tiles = ceil_div(pl.rows_pass, pl.wide ? pl.wide : 8 * pl.nt);
   pl.S = 0; pl.tps = 0;
   const int most = p.len.at ? c.Ncap : p.len.all;
   if (most > 0) {
-    const int64_t ctas = bh * tiles, sms = num_sms(), per_sm = kv8_ctas_per_sm(c.d, pl.nt, f32 ? 2 : 1);
-    const int64_t extra = 48 + 24 * pl.nt;       // tokens' worth of queries, join and partial results
+    const int64_t ctas = bh * tiles, sms = num_sms(), per_sm = pl.wide ? 1 : kv8_ctas_per_sm(c.d, pl.nt, f32 ? 2 : 1);
+    const int64_t extra = pl.wide ? 384 : 48 + 24 * pl.nt;       // tokens' worth of queries, join and partial results
     int64_t best = INT64_MAX;
     for (int S = 1, step = 1; S <= ceil_div(most, 128) && S <= 512; S += step) {
       if (S == 4 * step) step *= 2;              // 1, 2, 3, 4, 6, 8, 12, 16, ...
@@ -444,7 +447,7 @@ Kv8AttnPlan plan_kv8_attn(const lla_kv8_attn_params& p) {
     }
     pl.S = ceil_div(most, pl.tps);
   }
-  pl.tpc = 64;
+  pl.tpc = pl.wide ? 256 : 64;
   const int tail = !p.win_k ? 0 : p.tail.at ? p.Wcap : p.tail.all;
   pl.ST = pl.S + ceil_div(tail, pl.tpc);
   Carve v;
@@ -766,7 +769,7 @@ int lla_kv8_attn(const lla_kv8_attn_params* p, void* ws, size_t ws_bytes, lla_st
   std::memset(&a, 0, sizeof(a));
   a.p = *p;
   a.rows = p->nq * p->G;
-  a.rows_pass = pl.rows_pass; a.nt = pl.nt; a.S = pl.S; a.tps = pl.tps; a.ST = pl.ST; a.tpc = pl.tpc;
+  a.rows_pass = pl.rows_pass; a.nt = pl.nt; a.wide = pl.wide; a.S = pl.S; a.tps = pl.tps; a.ST = pl.ST; a.tpc = pl.tpc;
   a.direct = pl.ST == 1 && !p->weights;
   a.qmul = (p->scale > 0.f ? p->scale : 1.0f / std::sqrt((float)p->cache.d)) * kLog2e;
   char* w = static_cast<char*>(ws);

@@ -205,6 +205,17 @@ cudaError_t launch_absorb_split_tc(const AbsorbArgs& a, cudaStream_t st);
 // Per-sequence value: at[b], or all.
 __device__ __forceinline__ int kv8_at(const lla_i32& v, int b) { return v.at ? v.at[b] : v.all; }
 
+// 4 query elements at element offset `at`; zeros where !ok
+__device__ __forceinline__ void load_query(float (&x)[4], const void* q, int64_t at, int dtype, bool ok) {
+  if (dtype == LLA_BF16) {
+    const uint2 v = ok ? __ldg(reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(q) + at)) : make_uint2(0, 0);
+    x[0] = __uint_as_float(v.x << 16); x[1] = __uint_as_float(v.x & 0xffff0000u);
+    x[2] = __uint_as_float(v.y << 16); x[3] = __uint_as_float(v.y & 0xffff0000u);
+  } else {
+    const float4 v = ok ? __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(q) + at)) : make_float4(0, 0, 0, 0);
+    x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
+  }
+}
 // 4 elements times inv at element offset `at`
 __device__ __forceinline__ void store_quad(void* out, int64_t at, int dtype, float4 s, float inv) {
   if (dtype == LLA_BF16) {
@@ -226,6 +237,8 @@ struct Kv8AttnArgs {
   int rows, row0;          // query rows of a head (nq * G) that a launch serves, the first of them
   int rows_pass;           // most rows of one launch
   int nt;                  // row tiles of 8 that a CTA serves
+  int wide;                // cached splits go to the wide kernel, so many rows to a CTA (0: they do not)
+  int split0;              // first split of a launch
   int S, tps;              // splits of the cached tokens, tokens of each
   int ST, tpc;             // all splits: S, then those of the exact tokens, tpc tokens each
   int direct;              // one split and no weights: the split kernel writes the outputs itself
@@ -239,6 +252,8 @@ cudaError_t launch_kv8_attn(const Kv8AttnArgs& a, cudaStream_t st);
 __host__ __device__ constexpr int kv8_ctas_per_sm(int d, int nt, int terms) {
   return d > 128 ? (nt == 1 ? 2 : 1) : nt == 1 ? 4 : nt == 2 && terms == 1 ? 3 : 2;
 }
+// splits [0, S) for many rows (kv8_wide.cu): a.wide rows a CTA
+cudaError_t launch_kv8_wide(const Kv8AttnArgs& a, cudaStream_t st);
 // the split kernel of one code format and query type
 cudaError_t launch_kv8_attn_i8_bf16(const Kv8AttnArgs& a, cudaStream_t st);
 cudaError_t launch_kv8_attn_i8_f32(const Kv8AttnArgs& a, cudaStream_t st);

@@ -131,7 +131,11 @@ cudaError_t launch_kv8_attn(const Kv8AttnArgs& a0, cudaStream_t st) {
     a.row0 = row0;
     a.rows = total - row0 < a0.rows_pass ? total - row0 : a0.rows_pass;
     cudaError_t e = cudaSuccess;
-    if (a.ST > 0) {
+    if (a.wide && a.S) {
+      e = launch_kv8_wide(a, st);
+      a.split0 = a.S;
+    }
+    if (e == cudaSuccess && a.ST > a.split0) {
       const bool f32 = a.p.dtype == LLA_F32;
       if (c.code == LLA_KV8_I8) e = f32 ? launch_kv8_attn_i8_f32(a, st) : launch_kv8_attn_i8_bf16(a, st);
       else e = f32 ? launch_kv8_attn_e4m3_f32(a, st) : launch_kv8_attn_e4m3_bf16(a, st);

@@ -225,7 +225,7 @@ struct Place {
   int split, h, b, row0;
   int64_t bh;
   __device__ Place(const Kv8AttnArgs& a, int RT) {
-    split = blockIdx.x;
+    split = blockIdx.x + a.split0;
     h = blockIdx.y % a.p.cache.H;
     row0 = blockIdx.y / a.p.cache.H * RT;
     b = blockIdx.z;
@@ -310,18 +310,6 @@ __device__ __forceinline__ void join_store(const Kv8AttnArgs& a, Smem<D, NT, MT>
               make_float4(acc[2 * w][n][e], acc[2 * w][n][e + 2], acc[2 * w + 1][n][e], acc[2 * w + 1][n][e + 2]);
       }
     }
-}
-
-// A quad of 4 query elements.
-__device__ __forceinline__ void load_query(float (&x)[4], const void* q, int64_t at, int dtype, bool ok) {
-  if (dtype == LLA_BF16) {
-    const uint2 v = ok ? __ldg(reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(q) + at)) : make_uint2(0, 0);
-    const float2 a = unpack_bf16(v.x), b = unpack_bf16(v.y);
-    x[0] = a.x; x[1] = a.y; x[2] = b.x; x[3] = b.y;
-  } else {
-    const float4 v = ok ? __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(q) + at)) : make_float4(0, 0, 0, 0);
-    x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
-  }
 }
 
 // Nothing to see in this split: the join must not read what was there.
@@ -552,7 +540,7 @@ kv8_attn_kernel(const __grid_constant__ Kv8AttnArgs a) {
   griddep_wait();
   const lla_kv8_attn_params& p = a.p;
   const lla_kv8_cache& c = p.cache;
-  if ((int)blockIdx.x >= a.S) {
+  if ((int)blockIdx.x + a.split0 >= a.S) {
     if (p.win_dtype == LLA_BF16) exact_split<D, NT, MT, QT, 1>(a, sm);
     else exact_split<D, NT, MT, QT, 3>(a, sm);
     return;
@@ -848,7 +836,7 @@ cudaError_t launch_split(const Kv8AttnArgs& a, cudaStream_t st) {
     const cudaError_t e = allow_smem(kern, smem, done);
     if (e != cudaSuccess) return e;
   }
-  return launch_kernel(kern, dim3(a.ST, ceil_div(a.rows, 8 * NT) * c.H, c.B), dim3(AT), smem, st, 1, a);
+  return launch_kernel(kern, dim3(a.ST - a.split0, ceil_div(a.rows, 8 * NT) * c.H, c.B), dim3(AT), smem, st, 1, a);
 }
 
 // the planner chooses nt; a step of two tiles needs blocks of 32 tokens
