@@ -521,7 +521,7 @@ def _kv8_workspace(size, params, dev, workspace, stream):
         with cuda.device(dev):
             need = size(params)
     if need and workspace is None:
-        workspace = _torch().empty(need, dtype=_torch().uint8, device=f"cuda:{dev}")
+        workspace = _torch().empty(need, dtype=_torch().uint8, device=_torch().device("cuda", dev))
         if stream is not None:
             workspace.record_stream(stream)     # its memory is not handed out again before the call has run
     elif need and workspace.get_device() != dev:

@@ -62,18 +62,23 @@ cudaError_t launch_kernel(void (*kern)(Exp...), dim3 grid, dim3 block, size_t sm
   return cudaLaunchKernelEx(&cfg, kern, std::forward<Act>(args)...);
 }
 
-// Let kern use `smem` bytes of dynamic shared memory on the current device: set
-// once for each device, remembered in `done` (a bit for each device below 64).
+// Set a kernel's attribute on the current device: once for each, remembered in
+// `done` (a bit for each device below 64).
 template <typename Kern>
-cudaError_t allow_smem(Kern* kern, size_t smem, std::atomic<uint64_t>& done) {
+cudaError_t allow_once(Kern* kern, cudaFuncAttribute what, int value, std::atomic<uint64_t>& done) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   const uint64_t bit = dev >= 0 && dev < 64 ? uint64_t(1) << dev : 0;
   if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
-  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  e = cudaFuncSetAttribute(kern, what, value);
   if (e == cudaSuccess && bit) done.fetch_or(bit, std::memory_order_release);
   return e;
+}
+// Let kern use `smem` bytes of dynamic shared memory.
+template <typename Kern>
+cudaError_t allow_smem(Kern* kern, size_t smem, std::atomic<uint64_t>& done) {
+  return allow_once(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem, done);
 }
 
 constexpr float kLog2e = 1.4426950408889634f;

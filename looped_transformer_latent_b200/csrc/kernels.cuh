@@ -241,6 +241,7 @@ struct Kv8AttnArgs {
   int split0;              // first split of a launch
   int S, tps;              // splits of the cached tokens, tokens of each
   int ST, tpc;             // all splits: S, then those of the exact tokens, tpc tokens each
+  int cluster;             // all ST splits of a row tile are a cluster that joins them (0: they are not)
   int direct;              // one split and no weights: the split kernel writes the outputs itself
   float2* part_ml;         // [B][H][rows][ST] running maximum (base-2 exponent) and sum
   float* part_y;           // [B][H][rows][ST][d]

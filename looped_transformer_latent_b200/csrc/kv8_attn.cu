@@ -141,7 +141,7 @@ cudaError_t launch_kv8_attn(const Kv8AttnArgs& a0, cudaStream_t st) {
       else e = f32 ? launch_kv8_attn_e4m3_f32(a, st) : launch_kv8_attn_e4m3_bf16(a, st);
     }
     if (e != cudaSuccess) return e;
-    if (a.direct) continue;
+    if (a.direct || a.cluster) continue;
     const int wide = a.ST >= 8;                  // many splits: a CTA for each row shortens the chain of loads
     const int joins = wide ? a.rows : ceil_div(a.rows, AW);
     e = launch_kernel(kv8_join_kernel, dim3(joins + (a.p.weights ? ceil_div(c.Ncap, JT) : 0), c.H, c.B), dim3(AT), 0, st,

@@ -19,6 +19,7 @@
 #pragma once
 
 #include "kernels.cuh"
+#include "tc_ptx.cuh"
 
 namespace lla {
 namespace kv8 {
@@ -300,6 +301,15 @@ __device__ __forceinline__ void join_store(const Kv8AttnArgs& a, Smem<D, NT, MT>
                        make_float4(acc[2 * w][n][e], acc[2 * w][n][e + 2], acc[2 * w + 1][n][e], acc[2 * w + 1][n][e + 2]), inv);
         continue;
       }
+      if (a.cluster) {                           // for the other CTAs of the cluster to read (y[1] and ml[1] are done with)
+        if (g == 0) sm.ml[1][r - at_.row0] = make_float2(m[2 * n + e], l[2 * n + e]);
+#pragma unroll
+        for (int w = 0; w < D / 32; ++w)
+          if (base(w) < d)
+            *reinterpret_cast<float4*>(&sm.y[1][(r - at_.row0) * D + base(w)]) =
+                make_float4(acc[2 * w][n][e], acc[2 * w][n][e + 2], acc[2 * w + 1][n][e], acc[2 * w + 1][n][e + 2]);
+        continue;
+      }
       const int64_t at = (at_.bh * a.rows + r) * a.ST + at_.split;
       if (g == 0) a.part_ml[at] = make_float2(m[2 * n + e], l[2 * n + e]);
 #pragma unroll
@@ -314,7 +324,11 @@ __device__ __forceinline__ void join_store(const Kv8AttnArgs& a, Smem<D, NT, MT>
 
 // Nothing to see in this split: the join must not read what was there.
 template <int RT>
-__device__ __forceinline__ void empty_split(const Kv8AttnArgs& a, const Place& at) {
+__device__ __forceinline__ void empty_split(const Kv8AttnArgs& a, const Place& at, float2 (&ml)[2][RT]) {
+  if (a.cluster) {
+    if ((int)threadIdx.x < RT) ml[1][threadIdx.x] = make_float2(-INFINITY, 0.f);
+    return;
+  }
   if (a.direct) {
     for (int i = threadIdx.x; i < RT * (a.p.cache.d / 4); i += AT) {
       const int r = i / (a.p.cache.d / 4);
@@ -325,6 +339,51 @@ __device__ __forceinline__ void empty_split(const Kv8AttnArgs& a, const Place& a
   }
   if ((int)threadIdx.x < RT && at.row0 + (int)threadIdx.x < a.rows)
     a.part_ml[(at.bh * a.rows + at.row0 + threadIdx.x) * a.ST + at.split] = make_float2(-INFINITY, 0.f);
+}
+
+// Join of the splits of a cluster through its shared memory: a warp for each
+// row, the rows over the CTAs.  Lane k reads CTA k's maximum and sum; the loads
+// of all CTAs' y are under way together.
+template <int D, int NT, int MT>
+__device__ __forceinline__ void cluster_join(const Kv8AttnArgs& a, Smem<D, NT, MT>& sm) {
+  const Place at(a, 8 * NT);
+  const int d = a.p.cache.d, rows = min(8 * NT, a.rows - at.row0), lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  __syncthreads();
+  ptx::cluster_sync_all();
+  const uint32_t ml = smem_addr(sm.ml[1]), y = smem_addr(sm.y[1]);
+  for (int r = at.split * AW + warp; r < rows; r += a.ST * AW) {
+    float m = -INFINITY, l = 0.f;
+    if (lane < a.ST) {
+      const uint32_t x = ptx::mapa_shared(ml + 8 * r, lane);
+      m = ptx::ld_shared_cluster(x);
+      l = ptx::ld_shared_cluster(x + 4);
+    }
+    const unsigned some = __ballot_sync(0xffffffffu, !(m == -INFINITY && l == 0.f));   // an empty split wrote no y
+    const float top = warp_max(m), f = exp2f(m - (top == -INFINITY ? 0.f : top)), sum = warp_sum(l * f);
+    for (int e = 4 * lane; e - 4 * lane < d; e += 128) {
+      float4 s = make_float4(0, 0, 0, 0);
+#pragma unroll
+      for (int k0 = 0; k0 < 16; k0 += 8) {
+        float4 v[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          v[k] = make_float4(0, 0, 0, 0);
+          if (e < d && some >> (k0 + k) & 1)
+            asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+                         : "=f"(v[k].x), "=f"(v[k].y), "=f"(v[k].z), "=f"(v[k].w)
+                         : "r"(ptx::mapa_shared(y + 4 * (r * D + e), k0 + k)));
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const float g = __shfl_sync(0xffffffffu, f, k0 + k);
+          s.x += g * v[k].x; s.y += g * v[k].y; s.z += g * v[k].z; s.w += g * v[k].w;
+        }
+        if (k0 + 8 >= a.ST) break;
+      }
+      if (e < d) store_quad(a.p.out, at.output(a, r) + e, a.p.dtype, s, sum == 0.f ? 0.f : 1.f / sum);
+    }
+  }
+  ptx::cluster_sync_all();                       // a CTA's shared memory stays until all have read it
 }
 
 // ------------------------------------------------------------ exact tokens --
@@ -366,7 +425,7 @@ __device__ __noinline__ void exact_split(const Kv8AttnArgs& a, Smem<D, NT, MT>& 
   const int rows = min(RT, a.rows - at.row0);
   const int first = (at.split - a.S) * a.tpc;
   const int last = min(first + a.tpc, visible(tail, (a.row0 + at.row0 + rows - 1) / p.G, p.nq));
-  if (first >= last) { empty_split<RT>(a, at); return; }
+  if (first >= last) { empty_split<RT>(a, at, sm.ml); return; }
 
   for (int i = threadIdx.x; i < RT * (D / 4); i += AT) {
     const int r = i / (D / 4), w = i % (D / 4) / 4, tt = i % 4, e = quad_k(w, tt);
@@ -529,28 +588,19 @@ __device__ __noinline__ void exact_split(const Kv8AttnArgs& a, Smem<D, NT, MT>& 
 
 // ----------------------------------------------------------- cached tokens --
 template <int CODE, int D, int NT, int MT, int QT>
-__global__ void __launch_bounds__(AT, kv8_ctas_per_sm(D, NT, QT))
-kv8_attn_kernel(const __grid_constant__ Kv8AttnArgs a) {
+__device__ __forceinline__ void cached_split(const Kv8AttnArgs& a, Smem<D, NT, MT>& sm) {
   constexpr int RT = 8 * NT, STEP = 16 * MT, STAGES = Smem<D, NT, MT>::STAGES;
   constexpr int KW = D / 16, VW = D / 32;        // words per lane of a K and of a V row
   constexpr int PIECES = MT * (D / 16) / 2;      // 16-byte pieces of a stage that a lane copies
   using Wd = Widen<CODE>;
-  extern __shared__ __align__(128) uint8_t smem_raw[];
-  Smem<D, NT, MT>& sm = *reinterpret_cast<Smem<D, NT, MT>*>(smem_raw);
-  griddep_wait();
   const lla_kv8_attn_params& p = a.p;
   const lla_kv8_cache& c = p.cache;
-  if ((int)blockIdx.x + a.split0 >= a.S) {
-    if (p.win_dtype == LLA_BF16) exact_split<D, NT, MT, QT, 1>(a, sm);
-    else exact_split<D, NT, MT, QT, 3>(a, sm);
-    return;
-  }
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
   const Place at(a, RT);
   const int h = at.h, b = at.b;
   const int len = min(max(kv8_at(p.len, b), 0), c.Ncap);
   const int first = at.split * a.tps, last = min(len, first + a.tps);   // this split's tokens
-  if (first >= last) { empty_split<RT>(a, at); return; }
+  if (first >= last) { empty_split<RT>(a, at, sm.ml); return; }
 
   const uint8_t* kc = static_cast<const uint8_t*>(c.k) + (int64_t)b * c.stride_b + (int64_t)h * c.stride_h;
   const uint8_t* vc = static_cast<const uint8_t*>(c.v) + (int64_t)b * c.stride_b + (int64_t)h * c.stride_h;
@@ -827,16 +877,29 @@ kv8_attn_kernel(const __grid_constant__ Kv8AttnArgs a) {
 }
 
 template <int CODE, int D, int NT, int MT, int QT>
+__global__ void __launch_bounds__(AT, kv8_ctas_per_sm(D, NT, QT))
+kv8_attn_kernel(const __grid_constant__ Kv8AttnArgs a) {
+  extern __shared__ __align__(128) uint8_t smem_raw[];
+  Smem<D, NT, MT>& sm = *reinterpret_cast<Smem<D, NT, MT>*>(smem_raw);
+  griddep_wait();
+  if ((int)blockIdx.x + a.split0 < a.S) cached_split<CODE, D, NT, MT, QT>(a, sm);
+  else if (a.p.win_dtype == LLA_BF16) exact_split<D, NT, MT, QT, 1>(a, sm);
+  else exact_split<D, NT, MT, QT, 3>(a, sm);
+  if (a.cluster) cluster_join<D, NT, MT>(a, sm);
+}
+
+template <int CODE, int D, int NT, int MT, int QT>
 cudaError_t launch_split(const Kv8AttnArgs& a, cudaStream_t st) {
   const lla_kv8_cache& c = a.p.cache;
   constexpr size_t smem = sizeof(Smem<D, NT, MT>);
   auto* kern = kv8_attn_kernel<CODE, D, NT, MT, QT>;
-  static std::atomic<uint64_t> done{0};
-  if (smem > 48 * 1024) {
-    const cudaError_t e = allow_smem(kern, smem, done);
-    if (e != cudaSuccess) return e;
-  }
-  return launch_kernel(kern, dim3(a.ST - a.split0, ceil_div(a.rows, 8 * NT) * c.H, c.B), dim3(AT), smem, st, 1, a);
+  static std::atomic<uint64_t> done{0}, wide_clusters{0};
+  cudaError_t e = smem > 48 * 1024 ? allow_smem(kern, smem, done) : cudaSuccess;
+  if (e == cudaSuccess && a.cluster > 8)
+    e = allow_once(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1, wide_clusters);
+  if (e != cudaSuccess) return e;
+  return launch_kernel(kern, dim3(a.ST - a.split0, ceil_div(a.rows, 8 * NT) * c.H, c.B), dim3(AT), smem, st,
+                       a.cluster ? a.cluster : 1, a);
 }
 
 // the planner chooses nt; a step of two tiles needs blocks of 32 tokens
