@@ -464,6 +464,7 @@ typedef struct {
  * length, dst_len, is the old one less the evicted blocks' tokens.  Rows of dst
  * past it are left as they are, dst_weights from dst_len to the old length (as
  * far as dst reaches) is set to zero. */
+/* May be 0 (few heads, or `kept` given): ws is then not used. */
 size_t lla_kv8_evict_workspace_bytes(const lla_kv8_evict_params *p);
 int lla_kv8_evict(const lla_kv8_evict_params *p, void *ws, size_t ws_bytes, lla_stream stream);
 

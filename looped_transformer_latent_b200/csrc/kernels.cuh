@@ -261,11 +261,13 @@ cudaError_t launch_kv8_attn_i8_f32(const Kv8AttnArgs& a, cudaStream_t st);
 cudaError_t launch_kv8_attn_e4m3_bf16(const Kv8AttnArgs& a, cudaStream_t st);
 cudaError_t launch_kv8_attn_e4m3_f32(const Kv8AttnArgs& a, cudaStream_t st);
 
+// blocks of a head: the eviction holds a key and a place of each in shared memory
+constexpr int kv8_max_evict_blocks() { return 8192; }
 struct Kv8EvictArgs {
   lla_kv8_evict_params p;
   int inplace;
-  int* kept;               // [B][H][keep]
-  int2* info;              // [B] old and new length
+  int fused;               // one launch, a cluster for each head
+  int* kept;               // [B][H][keep] source blocks (two launches)
 };
 cudaError_t launch_kv8_evict(const Kv8EvictArgs& a, cudaStream_t st);
 

@@ -5,6 +5,7 @@
 #include <climits>
 
 #include "kernels.cuh"
+#include "tc_ptx.cuh"
 
 namespace lla {
 namespace {
@@ -217,7 +218,7 @@ cudaError_t launch_write(const lla_kv8_write_params& p, cudaStream_t st) {
 }
 
 // ---------------------------------------------------------------- eviction --
-constexpr int ST = 256;          // threads of the selection
+constexpr int ST = 256;          // threads of a CTA
 
 // Order-preserving map of fp32 to unsigned; NaN is the lowest.
 __device__ __forceinline__ uint32_t mass_key(float x) {
@@ -246,138 +247,229 @@ __device__ __forceinline__ int block_scan(int v, int* warp_sums, int* total) {  
   return before + x - v;
 }
 
-// One CTA chooses the blocks of one head: the sum of each block, then the
-// key of the lowest kept sum by four passes of an 8-bit histogram, then an
-// ordered scan.
-__global__ void __launch_bounds__(ST) kv8_select_kernel(const Kv8EvictArgs a) {
-  extern __shared__ uint32_t keys[];        // one per block
+constexpr int EC = 8;            // CTAs that move a head's blocks
+constexpr int MU = 8;            // blocks that a thread moves at a time
+
+// What becomes of a sequence.
+struct Cut {
+  int len, nb, left, nk;         // tokens, blocks; tokens that are left, blocks that stay
+  bool cut;
+  __device__ Cut(const lla_kv8_evict_params& p, int b) {
+    const int blk = p.src.block;
+    len = min(max(p.len[b], 0), p.src.Ncap);
+    nb = (len + blk - 1) / blk;
+    cut = nb > p.keep;
+    left = cut ? len - (nb - p.keep) * blk : len;
+    nk = cut ? p.keep : nb;
+  }
+};
+
+// Keys of blocks i, i + step, .. below hi by one warp, four blocks' loads under way at a time.
+__device__ __forceinline__ void block_keys(uint32_t* keys, const float* w, int i, int step, int hi, int blk) {
+  const int lane = threadIdx.x & 31;
+  for (; i < hi; i += 4 * step) {
+    double s[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      s[u] = 0.0;
+      if (i + u * step < hi)
+        for (int k = lane; k < blk; k += 32) s[u] += (double)w[(int64_t)(i + u * step) * blk + k];
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+      for (int u = 0; u < 4; ++u) s[u] += __shfl_xor_sync(0xffffffffu, s[u], o);
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (lane == u && i + u * step < hi) keys[i + u * step] = mass_key((float)s[u]);
+  }
+}
+
+// One CTA's choice among the candidates [lo, hi) by their keys: the lowest kept
+// key by four passes of an 8-bit histogram, then an ordered scan into `list`.
+__device__ __forceinline__ void choose_blocks(const lla_kv8_evict_params& p, const uint32_t* keys, int lo, int hi, int nb, int* list) {
   __shared__ int hist[256];
   __shared__ int sums[ST / 32];
   __shared__ uint32_t s_prefix;
   __shared__ int s_need;
-  griddep_wait();
-  const lla_kv8_evict_params& p = a.p;
-  const int h = blockIdx.x, b = blockIdx.y, blk = p.src.block;
-  const int len = min(max(p.len[b], 0), p.src.Ncap);
-  const int nb = (len + blk - 1) / blk;
-  int* kept = a.kept + ((int64_t)b * p.src.H + h) * p.keep;
-  if (h == 0 && threadIdx.x == 0)
-    a.info[b] = make_int2(len, nb <= p.keep ? len : len - (nb - p.keep) * blk);
-  if (nb <= p.keep) {
-    for (int i = threadIdx.x; i < p.keep; i += ST) kept[i] = i < nb ? i : -1;
-    return;
-  }
-  const float* w = p.weights + (int64_t)b * p.weights_stride_b + (int64_t)h * p.weights_stride_h;
-  const int lo = p.first, hi = nb - p.last;  // candidates [lo, hi): all of them whole blocks
-  for (int i = lo + threadIdx.x; i < hi; i += ST) {
-    double s = 0.0;
-    for (int j = 0; j < blk; ++j) s += (double)w[(int64_t)i * blk + j];
-    keys[i] = mass_key((float)s);
-  }
-  if (threadIdx.x == 0) { s_prefix = 0; s_need = p.keep - p.first - p.last; }
+  const int tid = threadIdx.x;
+  if (tid == 0) { s_prefix = 0; s_need = p.keep - p.first - p.last; }
+  __syncthreads();
   for (int shift = 24; shift >= 0; shift -= 8) {
-    hist[threadIdx.x] = 0;
+    hist[tid] = 0;
     __syncthreads();
     const uint32_t prefix = s_prefix;
     const int need = s_need;
-    for (int i = lo + threadIdx.x; i < hi; i += ST)
+    for (int i = lo + tid; i < hi; i += ST)
       if (shift == 24 || (keys[i] ^ prefix) >> (shift + 8) == 0) atomicAdd(&hist[keys[i] >> shift & 255], 1);
     __syncthreads();
     // how many keys lie in higher buckets than this thread's
     int total;
-    const int v = hist[255 - threadIdx.x];
+    const int v = hist[255 - tid];
     const int above = block_scan(v, sums, &total);
     if (need > 0 && above < need && above + v >= need) {
-      s_prefix = prefix | (uint32_t)(255 - threadIdx.x) << shift;
+      s_prefix = prefix | (uint32_t)(255 - tid) << shift;
       s_need = need - above;
     }
     __syncthreads();
   }
   const uint32_t edge = s_prefix;
-  const int ties = s_need;                  // keys equal to the edge that are kept, the lowest blocks first
+  const int ties = s_need;                     // keys equal to the edge that are kept, the lowest blocks first
   const bool any = p.keep > p.first + p.last;
   int at = 0, tied = 0;
   for (int i0 = 0; i0 < nb; i0 += ST) {
-    const int i = i0 + threadIdx.x;
+    const int i = i0 + tid;
     const bool cand = i >= lo && i < hi;
     const bool tie = any && cand && keys[i] == edge;
     int total;
-    const int rank = tied + block_scan(tie, sums, &total);
+    const int place = tied + block_scan(tie, sums, &total);
     tied += total;
-    const bool keep = i < nb && (!cand || (any && keys[i] > edge) || (tie && rank < ties));
+    const bool keep = i < nb && (!cand || (any && keys[i] > edge) || (tie && place < ties));
     const int to = at + block_scan(keep, sums, &total);
     at += total;
-    if (keep) kept[to] = i;
+    if (keep) list[to] = i;
   }
 }
 
-constexpr int MT = 128;          // threads of the move
-constexpr int MU = 8;            // blocks a CTA moves at a time
-
-// One CTA moves one 2 KB slice of every kept block of one head and part; the
-// last slice index moves the scales and weights.  Kept blocks stay in order,
-// so block i's source is at or after i: a CTA that reads MU blocks before it
-// writes them never reads what it has written, and slices share no byte.
-__global__ void __launch_bounds__(MT) kv8_move_kernel(const Kv8EvictArgs a, int slices) {
-  griddep_wait();
+// CTA `rank` of EC moves its own share of every kept block's K and V bytes.  Kept
+// blocks stay in order, so block i's source is at or after i: in place, a CTA
+// that reads a run of blocks before it writes them never reads what it has
+// written, and the CTAs' bytes are apart.  Ranks 0 to 2 move the scales and the
+// weights, too, which no CTA may still be reading.
+__device__ __forceinline__ void move_blocks(const Kv8EvictArgs& a, const Cut& c, int rank, int h, int b, const int* list) {
   const lla_kv8_evict_params& p = a.p;
-  const int h = blockIdx.y, b = blockIdx.z, blk = p.src.block, d = p.src.d;
-  const int* kept = a.kept + ((int64_t)b * p.src.H + h) * p.keep;
-  const int2 info = a.info[b];
-  const int nk = (info.y + blk - 1) / blk;  // blocks that stay
-  if ((int)blockIdx.x < 2 * slices) {
-    const int part = blockIdx.x / slices, off = (blockIdx.x % slices) * MT * 16 + threadIdx.x * 16;
-    const uint8_t* src = static_cast<const uint8_t*>(part ? p.src.v : p.src.k) + (int64_t)b * p.src.stride_b +
-                         (int64_t)h * p.src.stride_h;
-    uint8_t* dst = static_cast<uint8_t*>(part ? p.dst.v : p.dst.k) + (int64_t)b * p.dst.stride_b +
-                   (int64_t)h * p.dst.stride_h;
-    const int64_t unit = (int64_t)blk * d;
-    for (int i0 = 0; i0 < nk; i0 += MU) {
+  const int blk = p.src.block, d = p.src.d, nk = c.nk, left = c.left, len = c.len, tid = threadIdx.x;
+  if (a.inplace && !c.cut) return;
+  const float* w = p.weights + (int64_t)b * p.weights_stride_b + (int64_t)h * p.weights_stride_h;
+  // ---- K and V: the CTA's 16-byte pieces of a block, a thread to each and as many runs of blocks as threads allow
+  const int unit = blk * d / 16, all = 2 * unit, p0 = rank * all / EC, p1 = (rank + 1) * all / EC;
+  for (int q0 = p0; q0 < p1; q0 += ST) {
+    const int pieces = min(ST, p1 - q0), runs = ST / pieces, run = tid / pieces, q = q0 + tid % pieces;
+    const bool v = q >= unit;
+    const int off = 16 * (v ? q - unit : q);
+    const uint8_t* src = static_cast<const uint8_t*>(v ? p.src.v : p.src.k) + (int64_t)b * p.src.stride_b +
+                         (int64_t)h * p.src.stride_h + off;
+    uint8_t* dst = static_cast<uint8_t*>(v ? p.dst.v : p.dst.k) + (int64_t)b * p.dst.stride_b +
+                   (int64_t)h * p.dst.stride_h + off;
+    for (int i0 = 0; i0 < nk; i0 += runs * MU) {
       uint4 r[MU];
       bool go[MU];
 #pragma unroll
       for (int u = 0; u < MU; ++u) {
-        const int i = i0 + u;
+        const int i = i0 + run * MU + u;
         go[u] = false;
-        if (i < nk) {
-          const int s = kept[i];
-          const int64_t bytes = (int64_t)min(blk, info.y - i * blk) * d;
-          go[u] = off < bytes && !(a.inplace && s == i);
-          if (go[u]) r[u] = *reinterpret_cast<const uint4*>(src + s * unit + off);
+        if (run < runs && i < nk) {
+          const int s = list[i];
+          go[u] = off < min(blk, left - i * blk) * d && !(a.inplace && s == i);
+          if (go[u]) r[u] = *reinterpret_cast<const uint4*>(src + (int64_t)s * 16 * unit);
         }
       }
-      __syncthreads();
+      if (a.inplace) __syncthreads();            // all of the run's sources are read; what is written lies before the next's
 #pragma unroll
       for (int u = 0; u < MU; ++u)
-        if (go[u]) *reinterpret_cast<uint4*>(dst + (i0 + u) * unit + off) = r[u];
-      __syncthreads();
+        if (go[u]) *reinterpret_cast<uint4*>(dst + (int64_t)(i0 + run * MU + u) * 16 * unit) = r[u];
     }
-    return;
   }
-  const float* ss[2] = {p.src.k_scale, p.src.v_scale};
-  float* ds[2] = {p.dst.k_scale, p.dst.v_scale};
-  for (int part = 0; part < 2; ++part) {
-    const float* s = ss[part] + (int64_t)b * p.src.scale_stride_b + (int64_t)h * p.src.scale_stride_h;
-    float* t = ds[part] + (int64_t)b * p.dst.scale_stride_b + (int64_t)h * p.dst.scale_stride_h;
-    for (int i0 = 0; i0 < nk; i0 += MT) {
-      const int i = i0 + threadIdx.x;
-      const float x = i < nk ? s[kept[i]] : 0.f;
+  if (rank < 2) {                                // scales
+    const float* s = (rank ? p.src.v_scale : p.src.k_scale) + (int64_t)b * p.src.scale_stride_b + (int64_t)h * p.src.scale_stride_h;
+    float* t = (rank ? p.dst.v_scale : p.dst.k_scale) + (int64_t)b * p.dst.scale_stride_b + (int64_t)h * p.dst.scale_stride_h;
+    for (int i0 = 0; i0 < nk; i0 += ST) {
+      const int i = i0 + tid;
+      const float x = i < nk ? s[list[i]] : 0.f;
       __syncthreads();
       if (i < nk) t[i] = x;
       __syncthreads();
     }
+  } else if (rank == 2) {                        // weights
+    float* t = p.dst_weights + (int64_t)b * p.dst_weights_stride_b + (int64_t)h * p.dst_weights_stride_h;
+    constexpr int TU = 4;
+    for (int j0 = 0; j0 < left; j0 += TU * ST) {
+      float x[TU];
+#pragma unroll
+      for (int u = 0; u < TU; ++u) {
+        const int j = j0 + u * ST + tid;
+        x[u] = j < left ? w[(int64_t)list[j / blk] * blk + j % blk] : 0.f;
+      }
+      __syncthreads();
+#pragma unroll
+      for (int u = 0; u < TU; ++u) {
+        const int j = j0 + u * ST + tid;
+        if (j < left) t[j] = x[u];
+      }
+      __syncthreads();
+    }
+    for (int j = left + tid; j < min(len, p.dst.Ncap); j += ST) t[j] = 0.f;
   }
-  const float* w = p.weights + (int64_t)b * p.weights_stride_b + (int64_t)h * p.weights_stride_h;
-  float* t = p.dst_weights + (int64_t)b * p.dst_weights_stride_b + (int64_t)h * p.dst_weights_stride_h;
-  for (int j0 = 0; j0 < info.y; j0 += MT) {
-    const int j = j0 + threadIdx.x;
-    const float x = j < info.y ? w[(int64_t)kept[j / blk] * blk + j % blk] : 0.f;
+}
+
+// Few heads: a cluster of EC CTAs evicts from one head in one launch.  Its warps
+// sum the blocks' weights in turn, the keys go to all CTAs through the cluster's
+// shared memory, and each CTA makes the same choice for itself.
+__global__ void __launch_bounds__(ST) kv8_evict_kernel(const Kv8EvictArgs a) {
+  extern __shared__ uint32_t keys[];             // one per block, then the list of kept blocks
+  griddep_wait();
+  const lla_kv8_evict_params& p = a.p;
+  const int rank = blockIdx.x, h = blockIdx.y, b = blockIdx.z, tid = threadIdx.x, warp = tid >> 5;
+  const Cut c(p, b);
+  int* list = reinterpret_cast<int*>(keys + p.src.Ncap / p.src.block);
+  if (c.cut) {
+    const float* w = p.weights + (int64_t)b * p.weights_stride_b + (int64_t)h * p.weights_stride_h;
+    const int lo = p.first, hi = c.nb - p.last;  // candidates: all of them whole blocks
+    block_keys(keys, w, lo + rank + EC * warp, EC * (ST / 32), hi, p.src.block);
     __syncthreads();
-    if (j < info.y) t[j] = x;
+    ptx::cluster_sync_all();
+    for (int i = lo + tid; i < hi; i += ST) {
+      const int owner = (i - lo) % EC;
+      if (owner != rank)
+        keys[i] = __float_as_uint(ptx::ld_shared_cluster(ptx::mapa_shared((uint32_t)__cvta_generic_to_shared(keys + i), owner)));
+    }
     __syncthreads();
+    ptx::cluster_sync_all();                     // all have read: keys may go, weights may move
+    choose_blocks(p, keys, lo, hi, c.nb, list);
+  } else {
+    for (int i = tid; i < c.nb; i += ST) list[i] = i;
   }
-  for (int j = info.y + threadIdx.x; j < min(info.x, p.dst.Ncap); j += MT) t[j] = 0.f;
-  if (h == 0 && threadIdx.x == 0) p.dst_len[b] = info.y;
+  __syncthreads();
+  if (rank == 0) {
+    if (p.kept)
+      for (int i = tid; i < p.keep; i += ST) p.kept[((int64_t)b * p.src.H + h) * p.keep + i] = i < c.nk ? list[i] : -1;
+    if (h == 0 && tid == 0 && p.dst_len != p.len) p.dst_len[b] = c.left;
+  }
+  move_blocks(a, c, rank, h, b, list);
+}
+
+// Many heads: a CTA chooses for each, then EC CTAs move each head's blocks.
+__global__ void __launch_bounds__(ST) kv8_select_kernel(const Kv8EvictArgs a) {
+  extern __shared__ uint32_t keys[];
+  griddep_wait();
+  const lla_kv8_evict_params& p = a.p;
+  const int h = blockIdx.x, b = blockIdx.y, tid = threadIdx.x, warp = tid >> 5;
+  const Cut c(p, b);
+  int* list = a.kept + ((int64_t)b * p.src.H + h) * p.keep;
+  if (c.cut) {
+    const float* w = p.weights + (int64_t)b * p.weights_stride_b + (int64_t)h * p.weights_stride_h;
+    const int lo = p.first, hi = c.nb - p.last;
+    block_keys(keys, w, lo + warp, ST / 32, hi, p.src.block);
+    __syncthreads();
+    choose_blocks(p, keys, lo, hi, c.nb, list);
+  } else {
+    for (int i = tid; i < p.keep; i += ST) list[i] = i < c.nb ? i : -1;
+  }
+}
+__global__ void __launch_bounds__(ST) kv8_move_kernel(const Kv8EvictArgs a) {
+  griddep_wait();
+  const lla_kv8_evict_params& p = a.p;
+  const int rank = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
+  const Cut c(p, b);
+  if (rank == 0 && h == 0 && threadIdx.x == 0 && p.dst_len != p.len) p.dst_len[b] = c.left;
+  move_blocks(a, c, rank, h, b, a.kept + ((int64_t)b * p.src.H + h) * p.keep);
+}
+
+// Lengths in place: after every head has read them.
+__global__ void kv8_evict_len_kernel(const Kv8EvictArgs a) {
+  griddep_wait();
+  const int b = blockIdx.x * ST + threadIdx.x;
+  if (b < a.p.src.B) a.p.dst_len[b] = Cut(a.p, b).left;
 }
 
 }  // namespace
@@ -390,11 +482,18 @@ cudaError_t launch_kv8_write(const lla_kv8_write_params& p, cudaStream_t st) {
 
 cudaError_t launch_kv8_evict(const Kv8EvictArgs& a, cudaStream_t st) {
   const lla_kv8_cache& c = a.p.src;
-  const size_t smem = (size_t)(c.Ncap / c.block) * sizeof(uint32_t);
-  cudaError_t e = launch_kernel(kv8_select_kernel, dim3(c.H, c.B), dim3(ST), smem, st, 1, a);
-  if (e != cudaSuccess) return e;
-  const int slices = ceil_div(c.block * c.d, MT * 16);
-  return launch_kernel(kv8_move_kernel, dim3(2 * slices + 1, c.H, c.B), dim3(MT), 0, st, 1, a, slices);
+  const size_t keys = (size_t)(c.Ncap / c.block) * sizeof(uint32_t), smem = keys + a.p.keep * sizeof(int);
+  cudaError_t e = cudaSuccess;
+  if (a.fused) {
+    static std::atomic<uint64_t> done{0};
+    if (smem > 40 * 1024) e = allow_smem(kv8_evict_kernel, 2 * kv8_max_evict_blocks() * sizeof(uint32_t), done);
+    if (e == cudaSuccess) e = launch_kernel(kv8_evict_kernel, dim3(EC, c.H, c.B), dim3(ST), smem, st, EC, a);
+  } else {
+    e = launch_kernel(kv8_select_kernel, dim3(c.H, c.B), dim3(ST), keys, st, 1, a);
+    if (e == cudaSuccess) e = launch_kernel(kv8_move_kernel, dim3(EC, c.H, c.B), dim3(ST), 0, st, 1, a);
+  }
+  if (e != cudaSuccess || a.p.dst_len != a.p.len) return e;
+  return launch_kernel(kv8_evict_len_kernel, dim3(ceil_div(c.B, ST)), dim3(ST), 0, st, 1, a);
 }
 
 }  // namespace lla

@@ -383,6 +383,8 @@ EVICT = [  # B, H, d, block, lens, keep, first, last, code
     (3, 2, 128, 64, [0, 64, 1000], 5, 1, 1, "i8"), (2, 2, 96, 16, [481, 1], 7, 0, 3, "e4m3"),
     (1, 2, 256, 256, [2300], 3, 1, 2, "i8"), (1, 4, 48, 32, [900], 17, 2, 1, "i8"), (1, 1, 128, 16, [5003], 300, 1, 1, "i8"),
     (2, 1, 80, 16, [160, 161], 10, 4, 6, "e4m3"),
+    (40, 4, 16, 16, [16 * (i % 9) + i % 17 + (i == 3) * 900 for i in range(40)], 3, 0, 1, "i8"),      # many heads
+    (3, 60, 48, 32, [300, 0, 97], 2, 1, 1, "e4m3"),
 ]
 
 

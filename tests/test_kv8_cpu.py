@@ -179,13 +179,19 @@ def test_evict_refuses(p, status):
 
 
 def test_workspace_is_checked():
-    lib = L.lib()
-    for p, size, call in ((_attn(), lib.lla_kv8_attn_workspace_bytes, lib.lla_kv8_attn),
-                          (_evict(), lib.lla_kv8_evict_workspace_bytes, lib.lla_kv8_evict)):
-        need = size(ctypes.byref(p))
-        assert need > 0
-        for ws, nb in ((None, need), (FAKE, need - 1), (FAKE + 16, need)):
-            assert call(ctypes.byref(p), ws, nb, None) == _abi.LLA_ERR_WORKSPACE
+    lib, p = L.lib(), _attn()
+    need = lib.lla_kv8_attn_workspace_bytes(ctypes.byref(p))
+    assert need > 0
+    for ws, nb in ((None, need), (FAKE, need - 1), (FAKE + 16, need)):
+        assert lib.lla_kv8_attn(ctypes.byref(p), ws, nb, None) == _abi.LLA_ERR_WORKSPACE
+    assert lib.lla_kv8_evict_workspace_bytes(ctypes.byref(_evict())) == 0        # few heads
+    many = dict(B=200, stride_b=3 * 128 * 64, scale_stride_b=12)
+    p = _evict(many, many)
+    need = lib.lla_kv8_evict_workspace_bytes(ctypes.byref(p))
+    assert need >= 200 * 3 * 3 * 4
+    assert lib.lla_kv8_evict(ctypes.byref(p), None, need, None) == _abi.LLA_ERR_WORKSPACE
+    assert lib.lla_kv8_evict(ctypes.byref(p), FAKE, need - 1, None) == _abi.LLA_ERR_WORKSPACE
+    assert lib.lla_kv8_evict_workspace_bytes(ctypes.byref(_evict(many, many, kept=15 * FAKE))) == 0
 
 
 def test_empty_calls_do_nothing():
