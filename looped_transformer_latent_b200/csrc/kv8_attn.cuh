@@ -131,6 +131,9 @@ __device__ __forceinline__ uint32_t smem_addr(const void* p) { return (uint32_t)
 __device__ __forceinline__ void copy16(uint32_t to, const void* from, bool ok) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(ok ? 16 : 0) : "memory");
 }
+__device__ __forceinline__ void copy16(uint32_t to, const void* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
 __device__ __forceinline__ void copy4(uint32_t to, const void* from) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to), "l"(from) : "memory");
 }
@@ -405,8 +408,18 @@ __device__ __forceinline__ void load_quad(uint32_t (&o)[WT][2], const void* x, i
     for (int i = 0; i < WT; ++i) { o[i][0] = u[i]; o[i][1] = w[i]; }
   }
 }
-__device__ __forceinline__ bool no_number(uint32_t w) {   // of two bf16 (a term of an fp32 infinity is one, too)
-  return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
+// Whether one of 4 elements is an infinity or a NaN.
+template <int WT>
+__device__ __forceinline__ bool no_number(const void* x, int64_t at) {
+  if constexpr (WT == 1) {
+    const uint2 v = __ldg(reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(x) + at));
+    const uint32_t m = __vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu);
+    return (m & 0xffffu) >= 0x7f80u || m >= 0x7f800000u;
+  } else {
+    const uint4 v = __ldg(reinterpret_cast<const uint4*>(static_cast<const float*>(x) + at));
+    const uint32_t m = 0x7fffffffu;
+    return max(max(v.x & m, v.y & m), max(v.z & m, v.w & m)) >= 0x7f800000u;
+  }
 }
 
 // WT: terms of the ring's elements (bf16 1, fp32 3).  QT 1: bf16 queries, one
@@ -515,10 +528,8 @@ __device__ __noinline__ void exact_split(const Kv8AttnArgs& a, Smem<D, NT, MT>& 
       for (int w = 0; w < D / 32; ++w)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          uint32_t x[WT][2];
           const int e = quad_v<D>(w, g);
-          load_quad<WT>(x, p.win_v, vrow[i] + e, tb + 2 * t + (i & 1) + 8 * (i >> 1) < last && e < d);
-          odd |= no_number(x[0][0]) || no_number(x[0][1]);
+          odd |= tb + 2 * t + (i & 1) + 8 * (i >> 1) < last && e < d && no_number<WT>(p.win_v, vrow[i] + e);
         }
     if (!__any_sync(0xffffffffu, odd)) {
       uint32_t pt[NT][2][PB];
@@ -612,6 +623,14 @@ __device__ __forceinline__ void cached_split(const Kv8AttnArgs& a, Smem<D, NT, M
   auto copy_step = [&](int tb, int stage) {
     const uint32_t ks = smem_addr(sm.ring.kv[warp][stage][0]), vs = smem_addr(sm.ring.kv[warp][stage][1]);
     const uint8_t *kf = kc + (int64_t)tb * c.d, *vf = vc + (int64_t)tb * c.d;
+    if (c.d == D && tb + STEP <= last) {
+#pragma unroll
+      for (int i = 0; i < PIECES; ++i) {
+        const int id = lane + 32 * i, r = id / (D / 16), e = 16 * (id % (D / 16));
+        copy16(ks + Row<D>::at(r, e), kf + 16 * id);
+        copy16(vs + Row<D>::at(r, e), vf + 16 * id);
+      }
+    } else
 #pragma unroll
     for (int i = 0; i < PIECES; ++i) {
       const int id = lane + 32 * i, r = id / (D / 16), e = 16 * (id % (D / 16));
