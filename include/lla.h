@@ -361,7 +361,7 @@ typedef struct {
   int32_t B, H, d;         /* sequences, cache heads, head dim: a multiple of
                               16 up to 256                                      */
   int32_t block, Ncap;     /* tokens per scale (16, 32, 64, 128 or 256); rows
-                              per sequence, a multiple of block                 */
+                              per sequence, a multiple of block up to 2^30      */
   int32_t code;            /* lla_kv8_code                                      */
   void *k, *v;             /* codes [B, H, Ncap, d], rows dense                 */
   int64_t stride_b, stride_h;             /* multiples of 16; of a cache that a

@@ -330,7 +330,7 @@ int check_cache(const lla_kv8_cache& c) {
   if (c.d < 16 || c.d > 256 || c.d % 16) return LLA_ERR_UNSUPPORTED;
   if (c.block != 16 && c.block != 32 && c.block != 64 && c.block != 128 && c.block != 256) return LLA_ERR_UNSUPPORTED;
   if (c.Ncap % c.block) return LLA_ERR_SHAPE;
-  if (c.B > 32767 || c.H > 65535) return LLA_ERR_UNSUPPORTED;   // grid axes (the writer's holds 2 B)
+  if (c.B > 32767 || c.H > 65535 || c.Ncap > 1 << 30) return LLA_ERR_UNSUPPORTED;   // grid axes; 32-bit token numbers
   if (c.B == 0 || c.Ncap == 0) return LLA_OK;
   if (!c.k || !c.v || !c.k_scale || !c.v_scale) return LLA_ERR_NULL;
   if (!aligned(c.k, 16) || !aligned(c.v, 16) || c.stride_b % 16 || c.stride_h % 16) return LLA_ERR_ALIGN;
@@ -419,10 +419,10 @@ Kv8AttnPlan plan_kv8_attn(const lla_kv8_attn_params& p) {
   const lla_kv8_cache& c = p.cache;
   const int64_t bh = (int64_t)c.B * c.H;
   const int rows = p.nq * p.G;
-  pl.rows_pass = rows;
+  pl.rows_pass = (int)std::min<int64_t>(rows, 65535 / c.H * 16);   // a grid axis holds heads x row tiles (16 rows and more)
   if (p.weights && c.Ncap > 0) {
     const int64_t fit = (int64_t)(kScoreBytes / sizeof(float)) / (bh * c.Ncap) / 32 * 32;
-    pl.rows_pass = (int)std::min<int64_t>(rows, std::max<int64_t>(fit, 32));
+    pl.rows_pass = (int)std::min<int64_t>(pl.rows_pass, std::max<int64_t>(fit, 32));
   }
   // 32 rows of more than 128 elements, or with two terms of each, do not fit a thread's registers
   const bool f32 = p.dtype == LLA_F32;

@@ -290,6 +290,90 @@ def test_attention_large_logits_and_far_apart_scales():
             assert np.all(np.abs(got[r] - v64[0, s.argmax()]) <= 2.0 ** -7 * np.abs(v64[0, s.argmax()]))
 
 
+@pytest.mark.parametrize("d", [48, 96, 128])
+@pytest.mark.parametrize("G", [33, 64, 100, 160])
+def test_attention_of_many_rows_with_far_apart_scales(G, d):
+    """Rows beyond 32 go to the tcgen05 kernel; scales of values 2^-40 to 2^30 apart, one block zero, several splits."""
+    code = "i8" if G % 2 else "e4m3"
+    c = Cache(G, 2, 1, d, 32, 1312, code, [1300, 70])
+    w = torch.zeros(2, 1, 1312, device="cuda")
+    q = (2 * torch.randn(2, 1, G, d, generator=torch.Generator().manual_seed(1))).to(torch.bfloat16).cuda()
+    _check(c, q, _run_attn(c, q, weights=w), weights=w, before=torch.zeros_like(w))
+    f = torch.tensor([2.0 ** e for e in (0, -40, 5, -20, 30, 2, -3, 0, 1, -10)] * 5, device="cuda")[:41]
+    f[3] = 0
+    c.v_scale *= f
+    f = f.cpu().double().numpy()
+    c.values["v"] = [v * f[np.arange(v.shape[1]) // 32][None, :, None] for v in c.values["v"]]
+    _check(c, q, _run_attn(c, q))
+    # logits so far apart that one token has all the weight, wherever its block's scale lies
+    big = (100 * q.float()).to(torch.bfloat16)
+    got = _f64(_run_attn(c, big))
+    for b in range(2):
+        k, v = c.values["k"][b][0], c.values["v"][b][0]
+        for r in range(G):
+            s = k @ _f64(big)[b, 0, r] / math.sqrt(d)
+            top, second = np.sort(s)[::-1][:2]
+            # the others' shares are at most exp(second - top) each, on values up to the largest of all
+            rest = len(s) * math.exp(second - top) * np.abs(v).max()
+            if top - second > 60:
+                want = v[s.argmax()]
+                assert np.all(np.abs(got[b, 0, r] - want) <= 2.0 ** -7 * np.abs(want) + 2.0 ** -10 * np.abs(want).max() + 2 * rest)
+
+
+@pytest.mark.parametrize("G", [1, 40])
+def test_attention_keeps_what_a_query_does_not_see_out_of_it(G):
+    """A later position's value or key that is no number reaches that position's queries only."""
+    for wdt in ("bf16", "f32"):
+        c = Cache(3, 1, 2, 64, 32, 96, "i8", [70])
+        g = torch.Generator().manual_seed(1)
+        q = torch.randn(1, 3, 2 * G, 64, generator=g).to(torch.bfloat16).cuda()
+        win = [torch.randn(1, 8, 2, 64, generator=g).to(IO[wdt]).cuda() for _ in range(2)]
+        clean = _run_attn(c, q, win, [90], [6])
+        for ring, bad in ((1, math.inf), (1, math.nan), (0, math.nan)):
+            dirty = [x.clone() for x in win]
+            dirty[ring][0, 89 % 8, 1, 5] = bad           # the last position, head 1
+            out = _run_attn(c, q, dirty, [90], [6])
+            assert torch.equal(out[:, :2], clean[:, :2]) and torch.equal(out[:, 2, :G], clean[:, 2, :G])
+            assert not torch.isfinite(out[:, 2, G:]).all(-1).any()
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+def test_attention_of_more_heads_and_rows_than_a_grid_holds(io):
+    H, G, d = 30000, 300, 16                             # 3 or more row tiles of 30000 heads
+    g = torch.Generator(device="cuda").manual_seed(0)
+    k8, v8 = (torch.randint(-127, 128, (1, H, 16, d), generator=g, device="cuda", dtype=torch.int8) for _ in range(2))
+    s = torch.full((1, H, 1), 0.01, device="cuda")
+    q = torch.randn(1, 1, H * G, d, generator=g, device="cuda").to(IO[io])
+    out = torch.zeros_like(q)
+    L.lla_kv8_attn(q=q, out=out, lens=5, k8=k8, v8=v8, k_scale=s, v_scale=s)
+    for h0 in range(0, H, 10000):
+        at = slice(h0, h0 + 10000)
+        k, v = (x[0, at, :5].double() * 0.01 for x in (k8, v8))
+        a = torch.softmax(q[0, 0].view(H, G, d)[at].double() @ k.transpose(1, 2) / math.sqrt(d), -1)
+        # values up to 1.27; the bound on the rounding of a weight as above, and the output's own
+        err = (out[0, 0].view(H, G, d)[at].double() - a @ v).abs().max().item()
+        assert err <= 1.27 * ((2.0 ** -10 + 2.0 ** -8) if io == "bf16" else 2.0 ** -16)
+
+
+def test_weights_of_more_rows_than_one_pass_holds():
+    n, d, G = 1 << 20, 16, 96                            # scores of 64 rows fill a pass: two passes
+    g = torch.Generator(device="cuda").manual_seed(0)
+    k8, v8 = (torch.randint(-127, 128, (1, 1, n, d), generator=g, device="cuda", dtype=torch.int8) for _ in range(2))
+    ks, vs = (torch.rand(1, 1, n // 256, generator=g, device="cuda") * 0.01 + 0.01 for _ in range(2))
+    q = torch.randn(1, 1, G, d, generator=g, device="cuda").to(torch.bfloat16)
+    out, w = torch.empty_like(q), torch.zeros(1, 1, n, device="cuda")
+    m = n - 77
+    L.lla_kv8_attn(q=q, out=out, lens=m, k8=k8, v8=v8, k_scale=ks, v_scale=vs, weights=w)
+    k, v = (x[0, 0, :m].double() * s[0, 0].double().repeat_interleave(256)[:m, None] for x, s in ((k8, ks), (v8, vs)))
+    a = torch.softmax(q[0, 0].double() @ k.T / math.sqrt(d), -1)
+    ref = a @ v
+    top = (q[0, 0].double().abs() @ k.abs().T / math.sqrt(d)).max().item()
+    rel = 2 * top * (2.0 ** -22 + (d + 4) * 2.0 ** -24) + 2.0 ** -20 + 2.0 ** -24 * 4096   # longest run of one fp32 sum
+    assert ((out[0, 0].double() - ref).abs() <= v.abs().max() * (rel + 2.0 ** -10) + 2.0 ** -8 * ref.abs()).all()
+    want = a.sum(0)
+    assert ((w[0, 0, :m].double() - want).abs() <= (rel + 2.0 ** -20) * want + 1e-30).all() and not w[0, 0, m:].any()
+
+
 @pytest.mark.parametrize("code", ["i8", "e4m3"])
 def test_attention_of_a_block_of_nan_is_nan_in_its_head_only(code):
     c = Cache(4, 1, 2, 64, 16, 64, code, [50])

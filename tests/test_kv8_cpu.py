@@ -112,7 +112,7 @@ CACHE_FAULTS = [
     (dict(B=-1), "SHAPE"), (dict(H=0), "SHAPE"), (dict(Ncap=-32), "SHAPE"), (dict(Ncap=100), "SHAPE"),
     (dict(code=2), "DTYPE"), (dict(d=8), "UNSUPPORTED"), (dict(d=72), "UNSUPPORTED"), (dict(d=272), "UNSUPPORTED"),
     (dict(block=8), "UNSUPPORTED"), (dict(block=48), "UNSUPPORTED"), (dict(block=512), "UNSUPPORTED"),
-    (dict(B=40000), "UNSUPPORTED"), (dict(k=None), "NULL"), (dict(v=None), "NULL"), (dict(k_scale=None), "NULL"),
+    (dict(B=40000), "UNSUPPORTED"), (dict(H=70000), "UNSUPPORTED"), (dict(Ncap=(1 << 30) + 32), "UNSUPPORTED"), (dict(k=None), "NULL"), (dict(v=None), "NULL"), (dict(k_scale=None), "NULL"),
     (dict(v_scale=None), "NULL"), (dict(k=FAKE + 8), "ALIGN"), (dict(v=FAKE + 4), "ALIGN"),
     (dict(stride_b=3 * 128 * 64 + 8), "ALIGN"), (dict(stride_h=128 * 64 + 8), "ALIGN"),
     (dict(k_scale=2 * FAKE + 2), "ALIGN"), (dict(stride_b=-64), "SHAPE"), (dict(scale_stride_h=-1), "SHAPE"),
