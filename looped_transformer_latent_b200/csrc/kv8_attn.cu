@@ -1,5 +1,6 @@
 // Attention over the 8-bit K/V cache: join of the splits, weights, launches.
 #include "kernels.cuh"
+#include "tc_ptx.cuh"
 
 namespace lla {
 namespace {
@@ -104,12 +105,22 @@ __global__ void __launch_bounds__(AT) kv8_join_kernel(const __grid_constant__ Kv
       if (lane == 0) sml[r] = x;
     }
     __syncthreads();
-    for (int r = 0; r < n; ++r) {
+    // four rows' scores under way at a time; each token's terms are added in the rows' order
+    for (int r = 0; r < n; r += 4) {
       const float* s = a.scores + (bh * a.rows + r0 + r) * c.Ncap;
+      float x[4][JT / AT];
 #pragma unroll
-      for (int i = 0; i < JT / AT; ++i) {
-        const int j = j0 + threadIdx.x + AT * i;
-        if (j < len) sum[i] += exp2f(s[j] - sml[r].x) * sml[r].y;
+      for (int k = 0; k < 4; ++k)
+#pragma unroll
+        for (int i = 0; i < JT / AT; ++i) {
+          const int j = j0 + threadIdx.x + AT * i;
+          x[k][i] = r + k < n && j < len ? s[(int64_t)k * c.Ncap + j] : -INFINITY;
+        }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (r + k >= n) break;
+#pragma unroll
+        for (int i = 0; i < JT / AT; ++i) sum[i] += ptx::ex2(x[k][i] - sml[r + k].x) * sml[r + k].y;
       }
     }
   }

@@ -762,16 +762,20 @@ __device__ __forceinline__ void cached_split(const Kv8AttnArgs& a, Smem<D, NT, M
     // ---- logits (base 2); one beyond its reference moves that
     const float lv = __log2f(fabsf(vs));         // of a block of zeros -inf: never a rise
     const bool whole = tb + STEP <= last;
-    float cv[2 * NT];
+    float cv[2 * NT], keep_f[2 * NT], raw_s[MT][NT][4];
     bool rise = false;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       const float2 rf = *reinterpret_cast<const float2*>(&sm.rowf[8 * n + 2 * t]);
       const float f[2] = {rf.x * ks, rf.y * ks};
+      if (QT == 2) { keep_f[2 * n] = f[0]; keep_f[2 * n + 1] = f[1]; }
 #pragma unroll
       for (int m = 0; m < MT; ++m)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[m][n][e] *= f[e & 1];
+        for (int e = 0; e < 4; ++e) {
+          if (QT == 2) raw_s[m][n][e] = s[m][n][e];
+          s[m][n][e] *= f[e & 1];
+        }
     }
     if (!whole)
 #pragma unroll
@@ -817,7 +821,7 @@ __device__ __forceinline__ void cached_split(const Kv8AttnArgs& a, Smem<D, NT, M
           const float a1 = fmaxf(top + lv > a0 ? top + lv + kSlack : a0, fmaxf(m1 - 100.f, m1 + lv - 80.f));
           mo[i] = m1;
           ao[i] = a1;
-          F[i] = ex2(m1 - a1 + kSlack);
+          F[i] = ex2(QT == 1 ? m1 - a1 + kSlack : m1 - a1);
           cv[i] = vs * F[i];
           l[i] *= ex2(m0 - m1);
           const float r = ex2(a0 - a1);
@@ -834,9 +838,14 @@ __device__ __forceinline__ void cached_split(const Kv8AttnArgs& a, Smem<D, NT, M
         float w[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const float x = ex2(s[m][n][e] - mo[2 * n + (e & 1)]);
-          l[2 * n + (e & 1)] += x;
-          w[e] = x * cv[2 * n + (e & 1)];
+          // fp32: one rounding, of the difference to 2^kSlack below the reference, which is small where p is large
+          const int i = 2 * n + (e & 1);
+          float x;
+          if (QT == 1) x = ex2(s[m][n][e] - mo[i]);
+          else if (whole || s[m][n][e] > -INFINITY) x = ex2(fmaf(raw_s[m][n][e], keep_f[i], kSlack - mo[i]));
+          else x = s[m][n][e] == -INFINITY ? 0.f : s[m][n][e];
+          l[i] += x;
+          w[e] = x * cv[i];
         }
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -885,7 +894,7 @@ __device__ __forceinline__ void cached_split(const Kv8AttnArgs& a, Smem<D, NT, M
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const int i = 2 * n + e;
-      m[i] = mo[i] > kUnset ? mo[i] : -INFINITY;
+      m[i] = mo[i] > kUnset ? (QT == 1 ? mo[i] : mo[i] - kSlack) : -INFINITY;
 #pragma unroll
       for (int o = 4; o < 32; o <<= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], o);
       const float unit = 1.f / F[i];
