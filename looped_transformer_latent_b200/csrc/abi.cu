@@ -419,23 +419,25 @@ Kv8AttnPlan plan_kv8_attn(const lla_kv8_attn_params& p) {
   const lla_kv8_cache& c = p.cache;
   const int64_t bh = (int64_t)c.B * c.H;
   const int rows = p.nq * p.G;
-  pl.rows_pass = (int)std::min<int64_t>(rows, 65535 / c.H * 16);   // a grid axis holds heads x row tiles (16 rows and more)
+  pl.rows_pass = (int)std::min<int64_t>(rows, 65535 / c.H * 8);   // a grid axis holds heads x row tiles (8 rows and more)
   if (p.weights && c.Ncap > 0) {
     const int64_t fit = (int64_t)(kScoreBytes / sizeof(float)) / (bh * c.Ncap) / 32 * 32;
     pl.rows_pass = (int)std::min<int64_t>(pl.rows_pass, std::max<int64_t>(fit, 32));
   }
-  // 32 rows of more than 128 elements, or with two terms of each, do not fit a thread's registers
+  // 32 rows of more than 128 elements, or with two terms of each, do not fit a thread's registers.  fp32: two and three
+  // tiles of 8 rows take 55 and 82 us (64 heads of 96, up to 8000 tokens) where tiles of 16 take 84 and 94.  bf16, 512
+  // heads of 96, 4096 tokens: 16 rows 64 us in a tile of 16, 72 in two of 8.
   const bool f32 = p.dtype == LLA_F32;
-  pl.nt = pl.rows_pass <= 8 ? 1 : pl.rows_pass <= 16 || c.d > 128 || c.block < 32 || f32 ? 2 : 4;
-  // 33 rows and more (bf16, d <= 128): the tcgen05 kernel.  256 heads of 128, 4096 e4m3 tokens: 48 rows 143 us there
-  // and 179 in the mma.sync kernel, 128 rows 198 and 302; 32 rows 127 and 123, int8 heads of 96 125 and 119.
+  pl.nt = pl.rows_pass <= (f32 ? 24 : 8) ? 1 : pl.rows_pass <= 16 || c.d > 128 || c.block < 32 || f32 ? 2 : 4;
+  // 33 rows and more (bf16, d <= 128): the tcgen05 kernel.  256 heads, 4096 tokens, e4m3 of 128 / int8 of 96: 32 rows
+  // 138 / 139 us there and 86 / 82 in the mma.sync kernel, 48 rows 143 / 144 and 187 / 177, 128 rows 198 / 197 and 293 / 277.
   pl.wide = f32 || c.d > 128 || pl.rows_pass <= 32 ? 0 : pl.rows_pass <= 64 ? 64 : 128;
   const int tiles = ceil_div(pl.rows_pass, pl.wide ? pl.wide : 8 * pl.nt);
   pl.S = 0; pl.tps = 0;
   const int most = p.len.at ? c.Ncap : p.len.all;
   if (most > 0) {
     const int64_t ctas = bh * tiles, sms = num_sms(), per_sm = pl.wide ? 1 : kv8_ctas_per_sm(c.d, pl.nt, f32 ? 2 : 1);
-    const int64_t extra = pl.wide ? 384 : 48 + 24 * pl.nt;       // tokens' worth of queries, join and partial results
+    const int64_t extra = pl.wide ? 384 : 100 + 100 * pl.nt;   // tokens' worth of queries, join and partial results
     int64_t best = INT64_MAX;
     for (int S = 1, step = 1; S <= ceil_div(most, 128) && S <= 512; S += step) {
       if (S == 4 * step) step *= 2;              // 1, 2, 3, 4, 6, 8, 12, 16, ...
