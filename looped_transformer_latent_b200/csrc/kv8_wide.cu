@@ -14,6 +14,12 @@
 // are the other's work.
 // A row's reference is set kSlack above a new maximum; a tile whose logits pass
 // it is done again under a new one and the row's accumulators are rescaled.
+// Bound by shared memory and the softmax: a tile writes 64 KB of widened codes
+// and 32 KB of P and the products read 128 KB, 1800 cycles at 128 bytes each,
+// and 128 rows' exponentials take 1024.  256 heads of 128, 4096 e4m3 tokens: 48
+// rows 143 us, 128 rows 198 (348 TFLOP/s).  A softmax thread for each token instead of
+// each row (and rows walked in registers) took 170 and 270: it votes on every
+// tile and its sums do not fit registers.
 // Every wait is bounded; a CTA that gives up writes NaN.
 #include <type_traits>
 
