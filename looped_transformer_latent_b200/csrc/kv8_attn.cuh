@@ -431,6 +431,29 @@ __device__ __forceinline__ bool no_number(const void* x, int64_t at) {
   }
 }
 
+// s += the products of 16 elements, of WT terms on one side and YT on the other.
+// fp32 (QT 2): summed apart, the smallest terms first, and added to nearest: the
+// product unit's sums are not, and 48 of them in a row (heads of 128) shrank the
+// logits by 48 x 2^-25, an error of 3e-6 where a call's tokens were mostly exact.
+template <int QT, int WT, int YT, class Y>
+__device__ __forceinline__ void sum_terms(float (&s)[4], const uint32_t (&x)[WT][4], Y y) {
+  if constexpr (QT == 1) {
+#pragma unroll
+    for (int i = 0; i < WT; ++i)
+#pragma unroll
+      for (int k = 0; k < YT && i + k <= 2; ++k) mma_bf16(s, x[i], y(k).x, y(k).y);
+  } else {
+    float u[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int o = 2; o >= 0; --o)
+#pragma unroll
+      for (int i = 0; i < WT && i <= o; ++i)
+        if (o - i < YT) mma_bf16(u, x[i], y(o - i).x, y(o - i).y);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) s[e] += u[e];
+  }
+}
+
 // WT: terms of the ring's elements (bf16 1, fp32 3).  QT 1: bf16 queries, one
 // exact term, probabilities in two; QT 2: fp32, three of each.  Products of
 // terms whose order exceeds the third are left out: they are below 2^-24.
@@ -499,16 +522,15 @@ __device__ __noinline__ void exact_split(const Kv8AttnArgs& a, Smem<D, NT, MT>& 
       uint32_t x0[WT][2], x1[WT][2];
       load_quad<WT>(x0, p.win_k, k0 + e, ok0 && e < d);
       load_quad<WT>(x1, p.win_k, k1 + e, ok1 && e < d);
+      uint32_t op[WT][4];
 #pragma unroll
-      for (int i = 0; i < WT; ++i) {
-        const uint32_t op[4] = {x0[i][0], x1[i][0], x0[i][1], x1[i][1]};
+      for (int i = 0; i < WT; ++i) { op[i][0] = x0[i][0]; op[i][1] = x1[i][0]; op[i][2] = x0[i][1]; op[i][3] = x1[i][1]; }
 #pragma unroll
-        for (int k = 0; k < QB && i + k <= 2; ++k)
+      for (int n = 0; n < NT; ++n) {
+        uint2 q[QB];
 #pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            const uint2 q = sm.q[k][w][n][lane];
-            mma_bf16(s[n], op, q.x, q.y);
-          }
+        for (int k = 0; k < QB; ++k) q[k] = sm.q[k][w][n][lane];
+        sum_terms<QT, WT, QB>(s[n], op, [&](int k) { return q[k]; });
       }
     }
     float pr[NT][4];
@@ -524,8 +546,9 @@ __device__ __noinline__ void exact_split(const Kv8AttnArgs& a, Smem<D, NT, MT>& 
         for (int o = 4; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
         const float m1 = fmaxf(mo[i], top), f = ex2(mo[i] - m1);
         mo[i] = m1;
-        pr[n][e] = tb + g < vis[i] ? ex2(u - m1) : 0.f;
-        pr[n][e + 2] = tb + g + 8 < vis[i] ? ex2(v - m1) : 0.f;
+        // fp32: the difference to the reference is rounded once
+        pr[n][e] = tb + g < vis[i] ? ex2(QT == 1 ? u - m1 : fmaf(s[n][e], a.qmul, -m1)) : 0.f;
+        pr[n][e + 2] = tb + g + 8 < vis[i] ? ex2(QT == 1 ? v - m1 : fmaf(s[n][e + 2], a.qmul, -m1)) : 0.f;
         l[i] = l[i] * f + (pr[n][e] + pr[n][e + 2]);
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) { acc[k][n][e] *= f; acc[k][n][e + 2] *= f; }
@@ -560,13 +583,14 @@ __device__ __noinline__ void exact_split(const Kv8AttnArgs& a, Smem<D, NT, MT>& 
 #pragma unroll
         for (int k = 0; k < 2; ++k)
 #pragma unroll
-          for (int i = 0; i < WT; ++i) {
-            const uint32_t op[4] = {prmt(x[0][i][k], x[1][i][k], 0x5410), prmt(x[0][i][k], x[1][i][k], 0x7632),
-                                    prmt(x[2][i][k], x[3][i][k], 0x5410), prmt(x[2][i][k], x[3][i][k], 0x7632)};
+          for (int n = 0; n < NT; ++n) {
+            uint32_t op[WT][4];
 #pragma unroll
-            for (int o = 0; o < PB && i + o <= 2; ++o)
-#pragma unroll
-              for (int n = 0; n < NT; ++n) mma_bf16(acc[2 * w + k][n], op, pt[n][0][o], pt[n][1][o]);
+            for (int i = 0; i < WT; ++i) {
+              op[i][0] = prmt(x[0][i][k], x[1][i][k], 0x5410); op[i][1] = prmt(x[0][i][k], x[1][i][k], 0x7632);
+              op[i][2] = prmt(x[2][i][k], x[3][i][k], 0x5410); op[i][3] = prmt(x[2][i][k], x[3][i][k], 0x7632);
+            }
+            sum_terms<QT, WT, PB>(acc[2 * w + k][n], op, [&](int o) { return make_uint2(pt[n][0][o], pt[n][1][o]); });
           }
       }
       continue;

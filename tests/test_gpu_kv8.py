@@ -617,3 +617,29 @@ def test_a_serving_loop(code, io):
                         model[b][h][i][:] = [model[b][h][i][r] for r in rows]
                     assert np.array_equal(_f64(w[b, h, :keep * block]), np.array(model[b][h][2]))
             assert not w[:, :, keep * block:].any()
+
+
+@pytest.mark.parametrize("win", ["f32", "bf16"])
+@pytest.mark.parametrize("G,nq", [(1, 1), (8, 1), (2, 12), (32, 1)])
+@pytest.mark.parametrize("d", [64, 96, 128, 256])
+def test_f32_over_mostly_exact_tokens_keeps_its_precision(d, G, nq, win):
+    """The error of the whole output in norm, where the sums' own roundings show and not single elements.  Logits of
+    standard deviation 2: those that matter are about 4.5.  Added to nearest in D / 16 <= 16 steps a logit is off by
+    sqrt(16) 2^-24 / sqrt(3) 2.6 = 3.6e-7, by 2^-24 times the spread of 2 for the truncated sums of 16, by 2^-25 4.5 for
+    the rounding of the difference and 2^-22 / 3 for the exponential; the values' sum is off by less than the logits'.
+    Added up as squares that is 5e-7; twice that is allowed."""
+    B, H, W, T = 2, 3, 256, 250
+    c = Cache(11, B, H, d, 32, 32, "i8", [20, 3])
+    g = torch.Generator().manual_seed(d + G + nq)
+    q = (2 * torch.randn(B, nq, H * G, d, generator=g)).cuda()
+    ring = [torch.randn(B, W, H, d, generator=g).to(IO[win]).cuda() for _ in range(2)]
+    ctx = [1000, 77777]
+    out = _run_attn(c, q, ring, ctx, [T, T - 3])
+    err = norm = 0.0
+    for b, t in enumerate((T, T - 3)):
+        wk, wv = (kv8.ring_rows(_f64(x[b]), ctx[b], t).reshape(t, H, d) for x in ring)
+        ref, _ = kv8.attn(_f64(q[b]).reshape(nq, H, G, d), c.values["k"][b], c.values["v"][b], wk, wv)
+        got = _f64(out[b]).reshape(ref.shape)
+        err += np.sum((got - ref) ** 2)
+        norm += np.sum(ref ** 2)
+    assert math.sqrt(err / norm) <= 1e-6
