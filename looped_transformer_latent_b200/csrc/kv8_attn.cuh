@@ -22,7 +22,7 @@
 // instruction issue: of 1.9 instructions a cycle with 32 rows, a quarter are
 // products (33 % of the pipe), a quarter the softmax, a fifth the widening; 16 x
 // 55 heads of 96, 32 rows, 4096 int8 tokens take 235 us (3.0 TB/s).  fp32 queries
-// double the products and add their sums apart: 300 MB of 96-element heads in 90
+// double the products and add their sums apart: 300 MB of 96-element heads in 94
 // us.  Rings and not register prefetch: with 8 warps an SM the registers held
 // 24 KB under way, half of what the memory's latency asks for (462 us).
 #pragma once
