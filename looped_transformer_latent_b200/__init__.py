@@ -120,6 +120,16 @@ def _stream_handle(stream, device):
     return ctypes.c_void_p(s.cuda_stream)
 
 
+def _scratch(nbytes, device, stream):
+    """A call's scratch, taken from the allocator's blocks of the stream that the call runs on: whoever had the block
+    before or gets it next is ordered with the call by that stream."""
+    torch = _torch()
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
 def _workspace(nbytes, device, workspace):
     torch = _torch()
     if nbytes == 0:
@@ -521,9 +531,7 @@ def _kv8_workspace(size, params, dev, workspace, stream):
         with cuda.device(dev):
             need = size(params)
     if need and workspace is None:
-        workspace = _torch().empty(need, dtype=_torch().uint8, device=_torch().device("cuda", dev))
-        if stream is not None:
-            workspace.record_stream(stream)     # its memory is not handed out again before the call has run
+        workspace = _scratch(need, _torch().device("cuda", dev), stream)
     elif need and workspace.get_device() != dev:
         raise ValueError("workspace is on another device")
     if not need:

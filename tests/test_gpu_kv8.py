@@ -643,3 +643,52 @@ def test_f32_over_mostly_exact_tokens_keeps_its_precision(d, G, nq, win):
         err += np.sum((got - ref) ** 2)
         norm += np.sum(ref ** 2)
     assert math.sqrt(err / norm) <= 1e-6
+
+
+@pytest.mark.parametrize("many_heads", [False, True])
+def test_calls_on_two_streams_do_not_share_scratch(many_heads):
+    """Each stream's call takes its own scratch although neither waits for the other: reads with weights (partial results
+    and scores) and evictions of many heads (the list of blocks that stay)."""
+    B, H, d, block, cap = 4, 40, 64, 32, 1024
+    side, rounds = torch.cuda.Stream(), 20
+    sets = []
+    for seed in (1, 2):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        k8, v8 = (torch.randint(-127, 128, (B, H, cap, d), generator=g, device="cuda", dtype=torch.int8) for _ in range(2))
+        ks, vs = (torch.rand(B, H, cap // block, generator=g, device="cuda") * 0.02 for _ in range(2))
+        q = torch.randn(B, 3, H, d, generator=g, device="cuda").to(torch.bfloat16)
+        w = torch.rand(B, H, cap, generator=g, device="cuda")
+        sets.append((dict(k8=k8, v8=v8, k_scale=ks, v_scale=vs), q, w))
+
+    def buffers():
+        if not many_heads:
+            return [(torch.zeros_like(q), w.clone()) for _, q, w in sets]
+        return [dict({n: torch.zeros_like(t[:, :, :t.shape[2] // 4]) for n, t in c.items()},
+                     weights=torch.zeros(B, H, cap // 4, device="cuda"), lens=torch.zeros(B, dtype=torch.int32, device="cuda"))
+                for c, _, _ in sets]
+
+    def call(i, to, stream):
+        c, q, w = sets[i]
+        if many_heads:
+            L.lla_kv8_evict(**c, weights=w, lens=lens, keep=8, first=1, last=1, to=to, stream=stream)
+        else:
+            L.lla_kv8_attn(q=q, out=to[0], lens=lens, weights=to[1], stream=stream, **c)
+
+    lens = _i32([cap, cap - 5, 700, 900])
+    if many_heads:
+        assert L.lla_kv8_evict_workspace_bytes(**sets[0][0], weights=sets[0][2], lens=lens, keep=8) > 0
+    want = buffers()
+    for i in range(2):
+        call(i, want[i], None)
+        torch.cuda.synchronize()
+    got = [buffers() for _ in range(rounds)]
+    torch.cuda.synchronize()
+    for r in range(rounds):
+        call(0, got[r][0], None)
+        call(1, got[r][1], side)
+    torch.cuda.synchronize()
+    for r in range(rounds):
+        for i in range(2):
+            a, b = got[r][i], want[i]
+            for x, y in zip(a.values(), b.values()) if many_heads else zip(a, b):
+                assert torch.equal(x, y)

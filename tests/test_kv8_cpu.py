@@ -1,6 +1,7 @@
 """8-bit K/V cache without a GPU: the oracle against itself, and what the C ABI
 and the Python entry points refuse (a refused call returns before any CUDA call)."""
 
+import contextlib
 import ctypes
 import math
 
@@ -244,3 +245,33 @@ def test_python_binding_checks_shapes_and_dtypes(change, error):
     L._kv8_attn_params(**args)
     with pytest.raises(error):
         L._kv8_attn_params(**{**args, **change})
+
+
+class _Recorder:
+    """Stands in for torch.cuda.stream, torch.cuda.device and torch.empty: notes what is current where memory is taken."""
+
+    def __init__(self, monkeypatch):
+        self.now, self.taken = {"stream": None, "device": 0}, []
+        for what in ("stream", "device"):
+            monkeypatch.setattr(torch.cuda, what, lambda v, what=what: self._with(what, v))
+        monkeypatch.setattr(torch.cuda, "current_device", lambda: self.now["device"])
+        monkeypatch.setattr(torch, "empty", self._empty)
+
+    @contextlib.contextmanager
+    def _with(self, what, value):
+        before, self.now[what] = self.now[what], value
+        yield
+        self.now[what] = before
+
+    def _empty(self, n, dtype, device):
+        self.taken.append((n, device, self.now["stream"]))
+        return torch.zeros(n, dtype=dtype)
+
+
+def test_scratch_is_taken_on_the_stream_that_runs_the_call(monkeypatch):
+    rec, side = _Recorder(monkeypatch), object()
+    for stream in (None, side):
+        address, have, kept = L._kv8_workspace(lambda p: 512, None, 0, None, stream)
+        assert rec.taken.pop() == (512, torch.device("cuda", 0), stream)
+        assert address == kept.data_ptr() and have == 512
+    assert L._kv8_workspace(lambda p: 0, None, 0, None, side) == (None, 0, None) and not rec.taken
