@@ -130,15 +130,15 @@ def _scratch(nbytes, device, stream):
         return torch.empty(nbytes, dtype=torch.uint8, device=device)
 
 
-def _workspace(nbytes, device, workspace):
-    torch = _torch()
+def _workspace(nbytes, device, workspace, stream):
+    """(address, bytes, tensor) of a call's scratch; the caller holds the tensor until the call is issued."""
     if nbytes == 0:
-        return None, 0
+        return None, 0, None
     if workspace is None:
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        workspace = _scratch(nbytes, device, stream)
     if workspace.numel() * workspace.element_size() < nbytes:
         raise ValueError(f"workspace too small: {workspace.numel()} < {nbytes} bytes")
-    return ctypes.c_void_p(workspace.data_ptr()), workspace.numel() * workspace.element_size()
+    return ctypes.c_void_p(workspace.data_ptr()), workspace.numel() * workspace.element_size(), workspace
 
 
 def _call(fn, params, ws, nbytes, stream, where):
@@ -232,7 +232,7 @@ def lla_write_latents(mode, *, workspace=None, stream=None, **kw):
     p = _write_params(mode, **args)
     L = lib()
     need = L.lla_write_workspace_bytes(ctypes.byref(p))
-    ws, nb = _workspace(need, dev, workspace)
+    ws, nb, _keep = _workspace(need, dev, workspace, stream)
     _call(L.lla_write_latents, p, ws, nb, _stream_handle(stream, dev), "lla_write_latents")
 
 
@@ -355,7 +355,7 @@ def hla_decode_attn(*, workspace=None, stream=None, **kw):
     p = _hla_params(**args)
     L = lib()
     need = L.hla_decode_workspace_bytes(ctypes.byref(p))
-    ws, nb = _workspace(need, dev, workspace)
+    ws, nb, _keep = _workspace(need, dev, workspace, stream)
     _call(L.hla_decode_attn, p, ws, nb, _stream_handle(stream, dev), "hla_decode_attn")
 
 
@@ -415,7 +415,7 @@ def lla_decode_attn(*, workspace=None, stream=None, **kw):
     p = _lla_params(**args)
     L = lib()
     need = L.lla_decode_workspace_bytes(ctypes.byref(p))
-    ws, nb = _workspace(need, dev, workspace)
+    ws, nb, _keep = _workspace(need, dev, workspace, stream)
     _call(L.lla_decode_attn, p, ws, nb, _stream_handle(stream, dev), "lla_decode_attn")
 
 

@@ -210,3 +210,28 @@ def test_binding_refuses_cpu_tensors(lib):
         L.lla_write_latents(L.LLA_WRITE_HLA, x=x, E_main=torch.zeros(3, 256, 128),
                             E_1=torch.zeros(64, 128), out0=torch.zeros(1, 4, 256),
                             out1=torch.zeros(1, 4, 64), r_k=128, d_h=64)
+
+
+def test_scratch_is_taken_on_the_stream_that_runs_the_call(lib, monkeypatch):
+    from types import SimpleNamespace
+
+    import torch
+    taken, issued = [], []
+
+    def scratch(nbytes, device, stream):
+        taken.append(stream)
+        return torch.zeros(nbytes, dtype=torch.uint8)
+
+    monkeypatch.setattr(L, "_cuda", lambda *ts: torch.device("cuda", 0))
+    monkeypatch.setattr(L, "_scratch", scratch)
+    monkeypatch.setattr(L, "_call", lambda fn, p, ws, nb, stream, where: issued.append((where, stream.value)))
+    side = SimpleNamespace(cuda_stream=7)
+    f, z = torch.float32, torch.zeros
+    L.lla_write_latents(L.LLA_WRITE_HLA, stream=side, x=z(1, 2, 4, 128), E_main=z(3, 256, 128), E_1=z(64, 128),
+                        out0=z(1, 4, 256), out1=z(1, 4, 64), r_k=128, d_h=64)
+    L.hla_decode_attn(stream=side, lat=z(1, 64, 64, dtype=f), A=z(2, 2, 32, 32), Bm=z(2, 2, 32, 32), q=z(1, 2, 2, 32),
+                      win_k=z(1, 2, 8, 2, 32), win_v=z(1, 2, 8, 2, 32), out=z(1, 2, 2, 32), N=40, W=4)
+    L.lla_decode_attn(stream=side, cK=z(1, 2, 64, 16), cV=z(1, 2, 64, 16), UK=z(2, 2, 32, 16), UV=z(2, 2, 32, 16),
+                      q=z(1, 2, 2, 32), win_k=z(1, 2, 8, 2, 32), win_v=z(1, 2, 8, 2, 32), out=z(1, 2, 2, 32), N=40, W=4)
+    assert issued == [("lla_write_latents", 7), ("hla_decode_attn", 7), ("lla_decode_attn", 7)]
+    assert len(taken) == 3 and all(s is side for s in taken)
