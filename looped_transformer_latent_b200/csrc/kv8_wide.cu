@@ -13,7 +13,8 @@
 // take tiles in turn, each with its own scores, P and O, so that one's waits
 // are the other's work.
 // A row's reference is set kSlack above a new maximum; a tile whose logits pass
-// it is done again under a new one and the row's accumulators are rescaled.
+// it is done again under a new one, twice at most, and the row's accumulators
+// are rescaled.
 // Bound by shared memory and the softmax: a tile writes 64 KB of widened codes
 // and 32 KB of P and the products read 128 KB, 1800 cycles at 128 bytes each,
 // and 128 rows' exponentials take 1024.  256 heads of 128, 4096 e4m3 tokens: 48
@@ -41,7 +42,8 @@ constexpr int THREADS = 256 + CT + 64, PWARP = 8 + CT / 32;
 constexpr uint32_t TMEM_COLS = 512, O_COL = 256;   // two score tiles, two O
 constexpr int YP = 132;                        // pitch (floats) of the rows of O in the final join
 constexpr long long WAIT_CYCLES = 1ll << 32;   // about 2 s
-constexpr float kSlack = 12.f, kUnset = -1e30f;
+constexpr float kSlack = 12.f, kUnset = -3.4e38f;
+constexpr float kFar = 65536.f;                // beyond it a difference of references says nothing about a scale
 
 struct Smem {
   uint64_t rawfull[2], kfull, kfree, vfull, vfree, sfull[2], sfree[2], pfull[2], pfree[2], qfull, odone, fin[2];
@@ -77,6 +79,19 @@ __device__ __forceinline__ uint32_t e4m3_f16x2(uint32_t w) {
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// Two elements at a time, each rounded by itself (never one operation with the next).
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 r;
+  asm("{.reg .b64 a, b, r; mov.b64 a, {%2, %3}; mov.b64 b, {%4, %5}; mul.rn.f32x2 r, a, b; mov.b64 {%0, %1}, r;}"
+      : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 r;
+  asm("{.reg .b64 a, b, r; mov.b64 a, {%2, %3}; mov.b64 b, {%4, %5}; add.rn.f32x2 r, a, b; mov.b64 {%0, %1}, r;}"
+      : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
   return r;
 }
 __device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }
@@ -371,7 +386,9 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_wide_kernel(const __grid_const
     const int vex = max((int)(bar.vtop >> 23) - 127, -110);
     const float F = pow2(11 - vex);
     const bool far = bar.vtop > 0 && __uint_as_float(bar.vlow) < __uint_as_float(bar.vtop) * 0x1p-10f;
-    float m = kUnset, lf = 0.f, l = 0.f;         // reference, log2 of what P is multiplied by (far), sum
+    // references are whole numbers, so that moving one is exact; lf is kept by itself, so that it means the same
+    // however large the logits are
+    float m = kUnset, lf = 100.f, l = 0.f;       // reference, log2 of what P is multiplied by (far), sum
     bool ok = true;
     auto soft = [&](auto far_scales) {
       constexpr bool FAR = decltype(far_scales)::value;
@@ -389,11 +406,12 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_wide_kernel(const __grid_const
         __syncwarp();
         tc_fence_after();
         const uint32_t prow = smem_u32(p_s) + wg * TILE + at128 * 128;
-        // one turn over the tile's 32-token groups, the next one's scores on their way; MAX: only the maxima of the
-        // logits (under m = 0); ALL: every token is there
-        auto turn = [&](auto only_max, auto all, float& top, float& atop, float& sum) {
+        // one turn over the tile's 32-token groups, the next one's scores on their way; MAX: only the maxima (under
+        // m = 0); ALL: every token is there.  top: the largest logit; atop: the largest logit + log2 scale, less m;
+        // ltop: the largest log2 scale
+        auto turn = [&](auto only_max, auto all, float& top, float& atop, float& ltop, float& sum) {
           constexpr bool MAX = decltype(only_max)::value, ALL = decltype(all)::value;
-          const float ref = MAX ? 0.f : m;
+          const float ref = MAX ? 0.f : m, F1 = FAR ? ex2(lf) : F;
           auto group = [&](int g, float (&x)[32]) {
 #pragma unroll
             for (int hf = 0; hf < 32; hf += 16) {
@@ -401,33 +419,36 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_wide_kernel(const __grid_const
               const float f = __shfl_sync(0xffffffffu, scales, grp) * rowf, vs = __shfl_sync(0xffffffffu, scales, grp + 8);
               float t[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-              for (int i = 0; i < 16; ++i) {
-                float y = fmaf(x[hf + i], f, -ref);
-                if (!ALL && j0 + g + hf + i >= last) y = -INFINITY;
-                x[hf + i] = y;
-                t[i & 3] = fmaxf(t[i & 3], y);
+              for (int i = 0; i < 16; i += 2) {
+                // rounded, and not summed with m in one: no logit passes a reference above the largest
+                float2 y = mul2(make_float2(x[hf + i], x[hf + i + 1]), make_float2(f, f));
+                if (!ALL && j0 + g + hf + i >= last) y.x = -INFINITY;
+                if (!ALL && j0 + g + hf + i + 1 >= last) y.y = -INFINITY;
+                x[hf + i] = y.x; x[hf + i + 1] = y.y;
+                t[i & 2] = fmaxf(t[i & 2], y.x); t[i & 2 | 1] = fmaxf(t[i & 2 | 1], y.y);
               }
               const float most = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
               top = fmaxf(top, most);
               const float lv = FAR ? __log2f(fabsf(vs)) : 0.f;
-              if (FAR) atop = fmaxf(atop, most + lv);
+              if (FAR) { atop = fmaxf(atop, most - ref + lv); ltop = fmaxf(ltop, lv); }
               if (MAX) continue;
               if (a.scores && row < rows) {
                 float* to = a.scores + (bh * a.rows + row0 + row) * c.Ncap + j0 + g + hf;
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
-                  if (ALL || j0 + g + hf + i < last) to[i] = x[hf + i] + m;
+                  if (ALL || j0 + g + hf + i < last) to[i] = x[hf + i];
               }
-              const float vF = vs * F, sign = vs < 0.f ? -1.f : 1.f;
+              const float vF = vs * F1;
 #pragma unroll
               for (int i = 0; i < 16; i += 8) {
                 float w[8], part[2] = {0.f, 0.f};
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                  const float y = x[hf + i + k], e = ex2(y);
-                  part[k & 1] += e;
-                  if (FAR) w[k] = y == -INFINITY ? 0.f : vs == vs ? sign * ex2(y + (lf + lv)) : vs;
-                  else w[k] = ALL || y != -INFINITY ? e * vF : 0.f;   // a scale that is no number meets no absent token
+                for (int k = 0; k < 8; k += 2) {
+                  const float2 y = make_float2(x[hf + i + k], x[hf + i + k + 1]), s = add2(y, make_float2(-m, -m));
+                  const float2 e = make_float2(ex2(s.x), ex2(s.y)), v = mul2(e, make_float2(vF, vF));
+                  part[0] += e.x; part[1] += e.y;
+                  w[k] = ALL || y.x != -INFINITY ? v.x : 0.f;    // a scale that is no number meets no absent token
+                  w[k + 1] = ALL || y.y != -INFINITY ? v.y : 0.f;
                 }
                 sum += part[0] + part[1];
                 const int tk = c0 + g + hf + i;
@@ -450,29 +471,33 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_wide_kernel(const __grid_const
           }
         };
         if (n == wg) {                           // the first turn sets the references
-          float top = -INFINITY, atop = -INFINITY, none = 0.f;
-          if (whole) turn(std::true_type{}, std::true_type{}, top, atop, none);
-          else turn(std::true_type{}, std::false_type{}, top, atop, none);
+          float top = -INFINITY, atop = -INFINITY, ltop = -INFINITY, none = 0.f;
+          if (whole) turn(std::true_type{}, std::true_type{}, top, atop, ltop, none);
+          else turn(std::true_type{}, std::false_type{}, top, atop, ltop, none);
           if (top > -INFINITY) {
-            m = top + kSlack;
-            if (FAR) lf = fminf(m - atop, 100.f);        // w = exp2(s + log2 scale - a), a = m - lf: the largest is 1
+            m = ceilf(top) + kSlack;
+            // w = exp2(s + log2 scale - a), a = m - lf: the largest is 1
+            if (FAR && fabsf(m) < kFar) lf = fminf(m - ceilf(atop), fminf(100.f, 80.f - ltop));
           }
         }
-        while (true) {
-          float top = -INFINITY, atop = -INFINITY, sum = l;
-          if (whole) turn(std::false_type{}, std::true_type{}, top, atop, sum);
-          else turn(std::false_type{}, std::false_type{}, top, atop, sum);
-          if (!__any_sync(0xffffffffu, top > 0.f || (FAR && atop + lf > 14.f))) {
+        // At most two more turns: no logit passes the first new m, and under that atop is exact, so that the next lf holds.
+        for (int again = 2;; --again) {
+          float top = -INFINITY, atop = -INFINITY, ltop = -INFINITY, sum = l;
+          if (whole) turn(std::false_type{}, std::true_type{}, top, atop, ltop, sum);
+          else turn(std::false_type{}, std::false_type{}, top, atop, ltop, sum);
+          // scale * F stays finite: a probability of 0 may meet it
+          if (!__any_sync(0xffffffffu, top > m || (FAR && (atop + lf > 14.f || ltop + lf > 90.f))) || again == 0) {
             l = sum;
             break;
           }
-          const float m1 = top > 0.f ? m + top + kSlack : m;
-          float r = ex2(m - m1);
+          const float m1 = top > m ? ceilf(top) + kSlack : m, up = m1 - m;
+          float r = ex2(-up);
           l *= r;
           if (FAR) {
-            const float a0 = m - lf, v = m + atop, a1 = fmaxf(v > a0 + 12.f ? v : a0, m1 - 100.f);
-            lf = m1 - a1;
-            r = ex2(a0 - a1);
+            const float a = up < kFar ? (atop + lf > 14.f ? -ceilf(atop - up) : lf + up) : 100.f;
+            const float l1 = fminf(a, fminf(100.f, 80.f - ltop));
+            r = ex2(l1 - lf - up);
+            lf = l1;
           }
           m = m1;
           if (n > 1) {

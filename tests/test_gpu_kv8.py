@@ -692,3 +692,47 @@ def test_calls_on_two_streams_do_not_share_scratch(many_heads):
             a, b = got[r][i], want[i]
             for x, y in zip(a.values(), b.values()) if many_heads else zip(a, b):
                 assert torch.equal(x, y)
+
+
+def _one_hot(c, q, out, sc):
+    """Rows whose largest logit lies so far above the others, past what fp32 sums may be off by, that one token has all
+    the weight: those outputs.  How many there are."""
+    B, nq, HG, d = q.shape
+    H = c.k8.shape[1]
+    G, found = HG // H, 0
+    q64, o64 = _f64(q).reshape(B, nq, H, G, d), _f64(out).reshape(B, nq, H, G, d)
+    half = q.dtype == torch.bfloat16
+    for b, p, h, g in np.ndindex(B, nq, H, G):
+        k, v = c.values["k"][b][h], c.values["v"][b][h]
+        s = sc * (k @ q64[b, p, h, g])
+        off = sc * (np.abs(k) @ np.abs(q64[b, p, h, g])).max() * (2.0 ** -21 + (d + 4) * 2.0 ** -23)
+        top, second = np.sort(s)[::-1][:2]
+        if top - second > 2 * off + 60 and top < 1e38:
+            found += 1
+            # probabilities in f16 under the block's scale, the output's own rounding
+            tol = (2.0 ** -10 + 2.0 ** -8 if half else 2.0 ** -20) * np.abs(v[s.argmax()]).max()
+            assert np.all(np.abs(o64[b, p, h, g] - v[s.argmax()]) <= tol)
+    return found
+
+
+HUGE = [2.0 ** e for e in (12, 24, 27, 30, 40, 60, 90, 110)]
+
+
+@pytest.mark.parametrize("far", [False, True])
+@pytest.mark.parametrize("G", [40, 100])
+def test_many_rows_of_huge_logits_end_and_give_their_token(G, far):
+    """Logits past 2^29, where fp32 neighbours lie further apart than the references' slack."""
+    c = Cache(21, 2, 1, 64, 32, 320, "i8", [300, 140])
+    if far:
+        f = torch.tensor([2.0 ** e for e in (0, 20, -30, 5, 9, -12, 0, 3, -2, 1)], device="cuda")
+        c.v_scale *= f
+        c.values["v"] = [v * f.double().cpu().numpy()[np.arange(v.shape[1]) // 32][None, :, None] for v in c.values["v"]]
+    g = torch.Generator().manual_seed(2)
+    for factor in HUGE:
+        q = (factor * torch.randn(2, 1, G, 64, generator=g)).to(torch.bfloat16).cuda()
+        out = _run_attn(c, q)
+        assert torch.isfinite(out).all()
+        assert _one_hot(c, q, out, 1 / 8) >= G
+        w = torch.zeros(2, 1, 320, device="cuda")
+        _one_hot(c, q, _run_attn(c, q, weights=w), 1 / 8)
+        assert abs(w.sum().item() - 2 * G) <= 2 * G * 2.0 ** -12
