@@ -49,7 +49,8 @@ struct Smem {
   uint64_t rawfull[2], kfull, kfree, vfull, vfree, sfull[2], sfree[2], pfull[2], pfree[2], qfull, odone, fin[2];
   uint32_t tmem;
   int abort;
-  uint32_t qtop, vtop, vlow;                   // bits of the largest query element, largest and smallest value scale
+  uint32_t vtop, vlow;                         // bits of the largest and the smallest value scale
+  uint32_t qtop[128];                          // and of each query row's largest magnitude
 };
 
 __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatile int* abort) {
@@ -198,9 +199,10 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_wide_kernel(const __grid_const
     mbar_init(smem_u32(&bar.odone), 1);
     fence_mbar_init();
     bar.abort = 0;
-    bar.qtop = bar.vtop = 0;
+    bar.vtop = 0;
     bar.vlow = 0x7f800000u;
   }
+  if (tid < R) bar.qtop[tid] = 0;
   if (warp == PWARP) {
     tmem_alloc(smem_u32(&bar.tmem), TMEM_COLS);
     tmem_relinquish();
@@ -329,13 +331,15 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_wide_kernel(const __grid_const
     const int row = at128 % R, c0 = at128 / R * R;                    // row, first of its R tokens of a tile
     const uint32_t lanes = (uint32_t)(32 * q4) << 16;
     const uint32_t s_at = tmem + wg * TOK + c0 + lanes, o_at = tmem + O_COL + wg * 128 + lanes;
-    // ---- queries to f16 under one power of two that puts the largest element into [2^13, 2^14): a row 2^-k of the
-    // largest keeps its bits down to 2^-38 of that, far below what its logits need
+    // ---- queries to f16 under a power of two per row that puts the row's largest magnitude into [2^13, 2^14): each row
+    // keeps its bits whatever the others hold, and a row that is no number is its own
+    auto exponent = [](uint32_t top) {           // of a row; 0 where it is zero or no number
+      return top > 0 && top < 0x7f800000u ? max((int)(top >> 23) - 127 - 13, -100) : 0;
+    };
     uint32_t vt = 0, vl = 0x7f800000u;           // range of the value scales; zeros and what is no number do not count
     {
       constexpr int ALL = R * PC * 2, UNITS = (ALL + 255) / 256;    // pieces of 8 elements
       uint4 u[UNITS];
-      uint32_t top = 0;
 #pragma unroll
       for (int i = 0; i < UNITS; ++i) {
         const int id = tid + 256 * i, r = id / (PC * 2), e = 8 * (id % (PC * 2));
@@ -353,20 +357,18 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_wide_kernel(const __grid_const
       for (int i = 0; i < UNITS; ++i) {
         const uint32_t m = 0x7fff7fffu;
         const uint32_t w = __vmaxu2(__vmaxu2(u[i].x & m, u[i].y & m), __vmaxu2(u[i].z & m, u[i].w & m));
-        top = max(top, max(w << 16, w & 0xffff0000u));
+        if (w) atomicMax(&bar.qtop[(tid + 256 * i) / (PC * 2)], max(w << 16, w & 0xffff0000u));
       }
-      top = __reduce_max_sync(0xffffffffu, top);
       vt = __reduce_max_sync(0xffffffffu, vt);
       vl = __reduce_min_sync(0xffffffffu, vl);
-      if (lane == 0) { atomicMax(&bar.qtop, top); atomicMax(&bar.vtop, vt); atomicMin(&bar.vlow, vl); }
+      if (lane == 0) { atomicMax(&bar.vtop, vt); atomicMin(&bar.vlow, vl); }
       named_sync(1, 256);
-      const int qe = bar.qtop > 0 && bar.qtop < 0x7f800000u ? max((int)(bar.qtop >> 23) - 127 - 13, -100) : 0;
-      const float down = pow2(-qe);
 #pragma unroll
       for (int i = 0; i < UNITS; ++i) {
         const int id = tid + 256 * i, r = id / (PC * 2), k = id % (PC * 2);
         const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
         if (id >= ALL) break;
+        const float down = pow2(-exponent(bar.qtop[r]));
         uint32_t o[4];
 #pragma unroll
         for (int q = 0; q < 4; ++q)
@@ -379,8 +381,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_wide_kernel(const __grid_const
       fence_proxy_async_smem();
       mbar_arrive(smem_u32(&bar.qfull));
     }
-    const int ex = bar.qtop > 0 && bar.qtop < 0x7f800000u ? max((int)(bar.qtop >> 23) - 127 - 13, -100) : 0;
-    const float rowf = a.qmul * pow2(ex);
+    const float rowf = a.qmul * pow2(exponent(bar.qtop[row]));
     // probabilities (at most 1) are multiplied by scale * F <= 2^12; where a block's scale is less than 2^-10 of the
     // largest (far), by a reference of their own for each row instead, so that no block drowns another
     const int vex = max((int)(bar.vtop >> 23) - 127, -110);

@@ -736,3 +736,23 @@ def test_many_rows_of_huge_logits_end_and_give_their_token(G, far):
         w = torch.zeros(2, 1, 320, device="cuda")
         _one_hot(c, q, _run_attn(c, q, weights=w), 1 / 8)
         assert abs(w.sum().item() - 2 * G) <= 2 * G * 2.0 ** -12
+
+
+@pytest.mark.parametrize("G", [5, 40, 100])
+def test_a_row_does_not_depend_on_the_other_rows_queries(G):
+    """A padded row's query may hold anything: infinities, NaN, the type's largest value, values 2^60 times the others'."""
+    c = Cache(7, 1, 2, 96, 32, 320, "e4m3", [300])
+    q = torch.randn(1, 2, 2 * G, 96, generator=torch.Generator().manual_seed(3)).to(torch.bfloat16).cuda()
+    q[0, :, 1::2] *= 2.0 ** -12
+    clean = _run_attn(c, q)
+    _check(c, q, clean)
+    for bad in (math.nan, math.inf, -math.inf, torch.finfo(torch.bfloat16).max, 2.0 ** 60):
+        odd = q.clone()
+        odd[0, 1, 3] = bad
+        odd[0, 0, G + 2, 17] = bad
+        out = _run_attn(c, odd)
+        same = torch.ones(2, 2 * G, dtype=torch.bool)
+        same[1, 3] = same[0, G + 2] = False
+        assert torch.equal(out[0][same], clean[0][same])
+        if not math.isfinite(bad):
+            assert not torch.isfinite(out[0][~same]).all(-1).any()
