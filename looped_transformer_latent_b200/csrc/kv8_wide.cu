@@ -43,14 +43,15 @@ constexpr uint32_t TMEM_COLS = 512, O_COL = 256;   // two score tiles, two O
 constexpr int YP = 132;                        // pitch (floats) of the rows of O in the final join
 constexpr long long WAIT_CYCLES = 1ll << 32;   // about 2 s
 constexpr float kSlack = 12.f, kUnset = -3.4e38f;
+constexpr float kMost = 15.f, kHead = 3.f;     // log2 of the largest P, and of where a new lf puts it
+constexpr float kScale = kMost - 90.f;
 constexpr float kFar = 65536.f;                // beyond it a difference of references says nothing about a scale
 
 struct Smem {
   uint64_t rawfull[2], kfull, kfree, vfull, vfree, sfull[2], sfree[2], pfull[2], pfree[2], qfull, odone, fin[2];
   uint32_t tmem;
   int abort;
-  uint32_t vtop, vlow;                         // bits of the largest and the smallest value scale
-  uint32_t qtop[128];                          // and of each query row's largest magnitude
+  uint32_t qtop[128];                          // bits of each query row's largest magnitude
 };
 
 __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatile int* abort) {
@@ -199,8 +200,6 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_wide_kernel(const __grid_const
     mbar_init(smem_u32(&bar.odone), 1);
     fence_mbar_init();
     bar.abort = 0;
-    bar.vtop = 0;
-    bar.vlow = 0x7f800000u;
   }
   if (tid < R) bar.qtop[tid] = 0;
   if (warp == PWARP) {
@@ -336,7 +335,6 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_wide_kernel(const __grid_const
     auto exponent = [](uint32_t top) {           // of a row; 0 where it is zero or no number
       return top > 0 && top < 0x7f800000u ? max((int)(top >> 23) - 127 - 13, -100) : 0;
     };
-    uint32_t vt = 0, vl = 0x7f800000u;           // range of the value scales; zeros and what is no number do not count
     {
       constexpr int ALL = R * PC * 2, UNITS = (ALL + 255) / 256;    // pieces of 8 elements
       uint4 u[UNITS];
@@ -347,10 +345,6 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_wide_kernel(const __grid_const
                                                                           place(r, p.q_stride_b, p.q_stride_n) + e))
                                    : make_uint4(0, 0, 0, 0);
       }
-      for (int i = (first >> bshift) + tid; i <= (last - 1) >> bshift; i += 256) {
-        const uint32_t s = __float_as_uint(vsc[i]) & 0x7fffffffu;
-        if (s > 0 && s < 0x7f800000u) { vt = max(vt, s); vl = min(vl, s); }
-      }
       if (REP > 1)                               // P outside a copy's own tokens
         for (int i = tid; i < 2 * TILE / 16; i += 256) reinterpret_cast<uint4*>(p_s)[i] = make_uint4(0, 0, 0, 0);
 #pragma unroll
@@ -359,9 +353,6 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_wide_kernel(const __grid_const
         const uint32_t w = __vmaxu2(__vmaxu2(u[i].x & m, u[i].y & m), __vmaxu2(u[i].z & m, u[i].w & m));
         if (w) atomicMax(&bar.qtop[(tid + 256 * i) / (PC * 2)], max(w << 16, w & 0xffff0000u));
       }
-      vt = __reduce_max_sync(0xffffffffu, vt);
-      vl = __reduce_min_sync(0xffffffffu, vl);
-      if (lane == 0) { atomicMax(&bar.vtop, vt); atomicMin(&bar.vlow, vl); }
       named_sync(1, 256);
 #pragma unroll
       for (int i = 0; i < UNITS; ++i) {
@@ -382,17 +373,13 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_wide_kernel(const __grid_const
       mbar_arrive(smem_u32(&bar.qfull));
     }
     const float rowf = a.qmul * pow2(exponent(bar.qtop[row]));
-    // probabilities (at most 1) are multiplied by scale * F <= 2^12; where a block's scale is less than 2^-10 of the
-    // largest (far), by a reference of their own for each row instead, so that no block drowns another
-    const int vex = max((int)(bar.vtop >> 23) - 127, -110);
-    const float F = pow2(11 - vex);
-    const bool far = bar.vtop > 0 && __uint_as_float(bar.vlow) < __uint_as_float(bar.vtop) * 0x1p-10f;
-    // references are whole numbers, so that moving one is exact; lf is kept by itself, so that it means the same
-    // however large the logits are
-    float m = kUnset, lf = 100.f, l = 0.f;       // reference, log2 of what P is multiplied by (far), sum
+    // Probabilities p = exp2(s - m) <= 1 meet the codes times scale * F, F = 2^lf of the row: w = exp2(s + log2 scale - m
+    // + lf) <= 2^15 in f16, and the largest of them above 2^2 when lf is set, so that what f16 leaves out of the small
+    // ones (below 2^-24) stays 26 bits below the largest, whatever block that lies in.  References are whole numbers,
+    // so that moving one is exact; lf is kept by itself, so that it means the same however large the logits are.
+    float m = kUnset, lf = 0.f, l = 0.f;        // reference, log2 F, sum
     bool ok = true;
-    auto soft = [&](auto far_scales) {
-      constexpr bool FAR = decltype(far_scales)::value;
+    {
       // lanes 0-7 hold the K scales of a tile's groups of 16 tokens, 8-15 the V scales; read a turn ahead
       const float* sc = lane & 8 ? vsc : ksc;
       auto scale_of = [&](int n) { return __ldg(sc + (min(first + n * TOK + 16 * (lane & 7), last - 1) >> bshift)); };
@@ -408,11 +395,10 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_wide_kernel(const __grid_const
         tc_fence_after();
         const uint32_t prow = smem_u32(p_s) + wg * TILE + at128 * 128;
         // one turn over the tile's 32-token groups, the next one's scores on their way; MAX: only the maxima (under
-        // m = 0); ALL: every token is there.  top: the largest logit; atop: the largest logit + log2 scale, less m;
-        // ltop: the largest log2 scale
-        auto turn = [&](auto only_max, auto all, float& top, float& atop, float& ltop, float& sum) {
+        // m = 0); ALL: every token is there.  top: the largest logit; atop: the largest logit + log2 scale, less m
+        auto turn = [&](auto only_max, auto all, float& top, float& atop, float& sum) {
           constexpr bool MAX = decltype(only_max)::value, ALL = decltype(all)::value;
-          const float ref = MAX ? 0.f : m, F1 = FAR ? ex2(lf) : F;
+          const float F = ex2(lf);
           auto group = [&](int g, float (&x)[32]) {
 #pragma unroll
             for (int hf = 0; hf < 32; hf += 16) {
@@ -430,8 +416,8 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_wide_kernel(const __grid_const
               }
               const float most = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
               top = fmaxf(top, most);
-              const float lv = FAR ? __log2f(fabsf(vs)) : 0.f;
-              if (FAR) { atop = fmaxf(atop, most - ref + lv); ltop = fmaxf(ltop, lv); }
+              // kScale: scale * F stays below 2^90, as a probability of 0 may meet it
+              atop = fmaxf(atop, (MAX ? most : fmaxf(most - m, kScale)) + __log2f(fabsf(vs)));
               if (MAX) continue;
               if (a.scores && row < rows) {
                 float* to = a.scores + (bh * a.rows + row0 + row) * c.Ncap + j0 + g + hf;
@@ -439,7 +425,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_wide_kernel(const __grid_const
                 for (int i = 0; i < 16; ++i)
                   if (ALL || j0 + g + hf + i < last) to[i] = x[hf + i];
               }
-              const float vF = vs * F1;
+              const float vF = vs * F;
 #pragma unroll
               for (int i = 0; i < 16; i += 8) {
                 float w[8], part[2] = {0.f, 0.f};
@@ -472,35 +458,30 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_wide_kernel(const __grid_const
           }
         };
         if (n == wg) {                           // the first turn sets the references
-          float top = -INFINITY, atop = -INFINITY, ltop = -INFINITY, none = 0.f;
-          if (whole) turn(std::true_type{}, std::true_type{}, top, atop, ltop, none);
-          else turn(std::true_type{}, std::false_type{}, top, atop, ltop, none);
+          float top = -INFINITY, atop = -INFINITY, none = 0.f;
+          if (whole) turn(std::true_type{}, std::true_type{}, top, atop, none);
+          else turn(std::true_type{}, std::false_type{}, top, atop, none);
           if (top > -INFINITY) {
             m = ceilf(top) + kSlack;
-            // w = exp2(s + log2 scale - a), a = m - lf: the largest is 1
-            if (FAR && fabsf(m) < kFar) lf = fminf(m - ceilf(atop), fminf(100.f, 80.f - ltop));
+            lf = fabsf(m) < kFar ? fminf(kHead + m - ceilf(atop), 100.f) : 100.f;
           }
         }
-        // At most two more turns: no logit passes the first new m, and under that atop is exact, so that the next lf holds.
+        // At most two more turns: no logit passes the first new m, and under that atop is exact, so that the next lf
+        // holds.  Where m went up far, atop says nothing yet: lf takes its largest value, which the next turn sees.
         for (int again = 2;; --again) {
-          float top = -INFINITY, atop = -INFINITY, ltop = -INFINITY, sum = l;
-          if (whole) turn(std::false_type{}, std::true_type{}, top, atop, ltop, sum);
-          else turn(std::false_type{}, std::false_type{}, top, atop, ltop, sum);
-          // scale * F stays finite: a probability of 0 may meet it
-          if (!__any_sync(0xffffffffu, top > m || (FAR && (atop + lf > 14.f || ltop + lf > 90.f))) || again == 0) {
+          float top = -INFINITY, atop = -INFINITY, sum = l;
+          if (whole) turn(std::false_type{}, std::true_type{}, top, atop, sum);
+          else turn(std::false_type{}, std::false_type{}, top, atop, sum);
+          if (!__any_sync(0xffffffffu, top > m || atop + lf > kMost) || again == 0) {
             l = sum;
             break;
           }
           const float m1 = top > m ? ceilf(top) + kSlack : m, up = m1 - m;
-          float r = ex2(-up);
-          l *= r;
-          if (FAR) {
-            const float a = up < kFar ? (atop + lf > 14.f ? -ceilf(atop - up) : lf + up) : 100.f;
-            const float l1 = fminf(a, fminf(100.f, 80.f - ltop));
-            r = ex2(l1 - lf - up);
-            lf = l1;
-          }
+          const float l1 = fminf(up < kFar ? (atop + lf > kMost ? kHead - ceilf(atop - up) : lf + up) : 100.f, 100.f);
+          const float r = ex2(l1 - lf - up);
+          l *= ex2(-up);
           m = m1;
+          lf = l1;
           if (n > 1) {
 #pragma unroll 1
             for (int i = 0; i < 16 * PC; i += 16) {
@@ -519,9 +500,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_wide_kernel(const __grid_const
         fence_proxy_async_smem();
         mbar_arrive(smem_u32(&bar.pfull[wg]));
       }
-    };
-    if (far) soft(std::true_type{});
-    else soft(std::false_type{});
+    }
     ok = ok && wait_bar(&bar.odone, 0, abort);
     __syncwarp();
     tc_fence_after();
@@ -529,7 +508,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_wide_kernel(const __grid_const
     float* y_s = reinterpret_cast<float*>(k_s);          // [2][128][YP], then m and l of the 256 lanes
     float2* ml_s = reinterpret_cast<float2*>(y_s + 256 * YP);
     const bool some = wg < ntiles && m > kUnset;
-    const float unit = !some ? 0.f : far ? ex2(-lf) : pow2(vex - 11);
+    const float unit = some ? ex2(-lf) : 0.f;
     float* mine = y_s + tid * YP;
 #pragma unroll 1
     for (int i = 0; i < 16 * PC; i += 16) {

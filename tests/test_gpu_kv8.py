@@ -756,3 +756,33 @@ def test_a_row_does_not_depend_on_the_other_rows_queries(G):
         assert torch.equal(out[0][same], clean[0][same])
         if not math.isfinite(bad):
             assert not torch.isfinite(out[0][~same]).all(-1).any()
+
+
+@pytest.mark.parametrize("ratio", [0.9, 5, 60, 900, 1e6])
+@pytest.mark.parametrize("N", [700, 16384, 65536])
+@pytest.mark.parametrize("G", [32, 40, 100])
+def test_a_flat_rest_beside_a_peak_and_an_unattended_block(G, N, ratio):
+    """One token 14.4 bits above the rest, which together outweigh it, and a block whose values are `ratio` times the
+    others' and whose weight is nothing.  Probabilities are f16: 2^-11 each; those that f16 holds as subnormals, 2^-25
+    under a largest of 2^2 or more in one sum."""
+    d, block = 64, 64
+    g = torch.Generator().manual_seed(N)
+    k = torch.zeros(N, d, dtype=torch.int8)
+    k[0, 0] = 80
+    k[64:128, :2] = -127
+    v = torch.randint(-67, 128, (N, d), generator=g, dtype=torch.int8)
+    vs = torch.full((N // block + 1,), 0.01)
+    vs[1] *= ratio
+    q = torch.zeros(G, d)
+    q[:, :2] = 1 + torch.randint(-8, 9, (G, 2), generator=g) / 128
+    q = q.to(torch.bfloat16)
+    cap = (N // block + 1) * block
+    k8, v8 = (torch.nn.functional.pad(x, (0, 0, 0, cap - N))[None, None].cuda() for x in (k, v))
+    out = torch.zeros(1, 1, G, d, dtype=torch.bfloat16, device="cuda")
+    L.lla_kv8_attn(q=q[None, None].cuda(), out=out, lens=N, k8=k8, v8=v8, k_scale=torch.ones(1, 1, len(vs), device="cuda"),
+                   v_scale=vs[None, None].cuda())
+    val = v.double() * vs.double()[torch.arange(N) // block, None]
+    a = torch.softmax(q.double() @ k.double().T / math.sqrt(d), -1)
+    ref = a @ val
+    bound = a @ val.abs() * 2.0 ** -10 + a[:, :1] * 1.27 * N * 2.0 ** -27 + ref.abs() * 2.0 ** -8
+    assert ((out[0, 0].double().cpu() - ref).abs() <= bound).all()
