@@ -210,9 +210,14 @@ constexpr int kQExp = 13;
 // p = exp2(s - m), a of what meets the value codes, w = 2^12 exp2(s + log2(scale) - a),
 // so that a block whose values are 2^60 times another's does not drown it.  A
 // reference is set kSlack above a new maximum and moves only when a logit
-// exceeds it: p <= 1, w <= 2^12 in f16 and the largest of them above 2^-4, and
-// most tiles need neither a shuffle nor a rescaling.
-constexpr float kSlack = 12.f, kUnset = -1e30f;
+// exceeds it: p <= 1, w <= 2^12 in f16 and the largest of them above 2^-1, and
+// most tiles need neither a shuffle nor a rescaling.  References are whole
+// numbers, so that moving one is exact, and of a only m - a is kept, which means
+// the same however large the logits are.
+constexpr float kSlack = 12.f, kUnset = -3.4e38f;
+// from here on the rounding of a product exceeds the slack of f16, and the difference to a reference is taken from
+// the rounded logit, which lies below it
+constexpr float kHuge = 16777216.f;
 
 
 // MT: tiles of 16 tokens that a warp takes at a time.
@@ -539,16 +544,17 @@ __device__ __noinline__ void exact_split(const Kv8AttnArgs& a, Smem<D, NT, MT>& 
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int i = 2 * n + e;
-        const float u = tb + g < vis[i] ? s[n][e] * a.qmul : -INFINITY;
-        const float v = tb + g + 8 < vis[i] ? s[n][e + 2] * a.qmul : -INFINITY;
+        const float u = tb + g < vis[i] ? __fmul_rn(s[n][e], a.qmul) : -INFINITY;
+        const float v = tb + g + 8 < vis[i] ? __fmul_rn(s[n][e + 2], a.qmul) : -INFINITY;
         float top = fmaxf(u, v);
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
         const float m1 = fmaxf(mo[i], top), f = ex2(mo[i] - m1);
         mo[i] = m1;
         // fp32: the difference to the reference is rounded once
-        pr[n][e] = tb + g < vis[i] ? ex2(QT == 1 ? u - m1 : fmaf(s[n][e], a.qmul, -m1)) : 0.f;
-        pr[n][e + 2] = tb + g + 8 < vis[i] ? ex2(QT == 1 ? v - m1 : fmaf(s[n][e + 2], a.qmul, -m1)) : 0.f;
+        const bool once = QT == 2 && fabsf(m1) < kHuge;
+        pr[n][e] = tb + g < vis[i] ? ex2(once ? fmaf(s[n][e], a.qmul, -m1) : u - m1) : 0.f;
+        pr[n][e + 2] = tb + g + 8 < vis[i] ? ex2(once ? fmaf(s[n][e + 2], a.qmul, -m1) : v - m1) : 0.f;
         l[i] = l[i] * f + (pr[n][e] + pr[n][e + 2]);
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) { acc[k][n][e] *= f; acc[k][n][e + 2] *= f; }
@@ -722,7 +728,8 @@ __device__ __forceinline__ void cached_split(const Kv8AttnArgs& a, Smem<D, NT, M
   __syncthreads();
 
   float acc[D / 16][NT][4];
-  float mo[2 * NT], ao[2 * NT], F[2 * NT], l[2 * NT];   // references, F = 2^12 exp2(mo - ao), sums
+  float mo[2 * NT], da[2 * NT], F[2 * NT], l[2 * NT];   // reference m, m - a, F = 2^12 exp2(m - a), sums
+  bool huge = false;                                    // the warp has seen an |m| >= kHuge
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -731,7 +738,7 @@ __device__ __forceinline__ void cached_split(const Kv8AttnArgs& a, Smem<D, NT, M
       for (int e = 0; e < 4; ++e) acc[i][n][e] = 0.f;
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      mo[2 * n + e] = ao[2 * n + e] = kUnset; F[2 * n + e] = 1.f; l[2 * n + e] = 0.f;
+      mo[2 * n + e] = kUnset; da[2 * n + e] = 0.f; F[2 * n + e] = 1.f; l[2 * n + e] = 0.f;
     }
   }
 
@@ -807,7 +814,7 @@ __device__ __forceinline__ void cached_split(const Kv8AttnArgs& a, Smem<D, NT, M
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           if (QT == 2) raw_s[m][n][e] = s[m][n][e];
-          s[m][n][e] *= f[e & 1];
+          s[m][n][e] = __fmul_rn(s[m][n][e], f[e & 1]);
         }
     }
     if (!whole)
@@ -820,9 +827,10 @@ __device__ __forceinline__ void cached_split(const Kv8AttnArgs& a, Smem<D, NT, M
             if (tb + 16 * m + g + 8 * (e >> 1) >= last) s[m][n][e] = -INFINITY;
 #pragma unroll
     for (int i = 0; i < 2 * NT; ++i) {
-      const float edge = fminf(mo[i], ao[i] - lv);
+      float most = fmaxf(s[0][i / 2][i % 2], s[0][i / 2][i % 2 + 2]);
 #pragma unroll
-      for (int m = 0; m < MT; ++m) rise |= fmaxf(s[m][i / 2][i % 2], s[m][i / 2][i % 2 + 2]) > edge;
+      for (int m = 1; m < MT; ++m) most = fmaxf(most, fmaxf(s[m][i / 2][i % 2], s[m][i / 2][i % 2 + 2]));
+      rise |= most - mo[i] > fminf(0.f, -da[i] - lv);
       cv[i] = vs * F[i];
       rise |= cv[i] > 1e30f;                     // kept finite: a probability of 0 may meet it
     }
@@ -848,18 +856,37 @@ __device__ __forceinline__ void cached_split(const Kv8AttnArgs& a, Smem<D, NT, M
           for (int m = 0; m < MT; ++m) top = fmaxf(top, fmaxf(s[m][n][e], s[m][n][e + 2]));
 #pragma unroll
           for (int o = 4; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-          const float m0 = mo[i], a0 = ao[i];
-          const float m1 = top > m0 ? top + kSlack : m0;
+          const bool over = top > mo[i];
+          const float m1 = over ? ceilf(top) + kSlack : mo[i], up = over ? m1 - mo[i] : 0.f;
+          const float a0 = -da[i] - up, v = top - m1 + lv;     // a, and the tile's largest s + log2(scale), less m1
           // F vs stays below 2^100 and F below 2^112: blocks of tiny values lie at most 2^100 below
-          const float a1 = fmaxf(top + lv > a0 ? top + lv + kSlack : a0, fmaxf(m1 - 100.f, m1 + lv - 80.f));
+          const float a1 = fmaxf(v > a0 ? ceilf(v) + kSlack : a0, fmaxf(-100.f, ceilf(lv) - 80.f));
           mo[i] = m1;
-          ao[i] = a1;
-          F[i] = ex2(QT == 1 ? m1 - a1 + kSlack : m1 - a1);
+          da[i] = -a1;
+          huge |= QT == 2 && fabsf(m1) >= kHuge;
+          F[i] = ex2(QT == 1 ? kSlack - a1 : -a1);
           cv[i] = vs * F[i];
-          l[i] *= ex2(m0 - m1);
+          l[i] *= ex2(-up);
           const float r = ex2(a0 - a1);
 #pragma unroll
           for (int k = 0; k < D / 16; ++k) { acc[k][n][e] *= r; acc[k][n][e + 2] *= r; }
+        }
+      if (QT == 2) huge = __any_sync(0xffffffffu, huge);
+    }
+    float ref[2 * NT];
+    if (QT == 2) {
+#pragma unroll
+      for (int i = 0; i < 2 * NT; ++i) ref[i] = kSlack - mo[i];
+      if (huge)
+#pragma unroll
+        for (int i = 0; i < 2 * NT; ++i) {
+          const bool h = fabsf(mo[i]) >= kHuge;
+          if (h) { keep_f[i] = 1.f; ref[i] = kSlack; }
+#pragma unroll
+          for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int e = i % 2; e < 4; e += 2)
+              if (h) raw_s[m][i / 2][e] = s[m][i / 2][e] - mo[i];
         }
     }
     // ---- P, and O^T += V^T P^T
@@ -875,7 +902,7 @@ __device__ __forceinline__ void cached_split(const Kv8AttnArgs& a, Smem<D, NT, M
           const int i = 2 * n + (e & 1);
           float x;
           if (QT == 1) x = ex2(s[m][n][e] - mo[i]);
-          else if (whole || s[m][n][e] > -INFINITY) x = ex2(fmaf(raw_s[m][n][e], keep_f[i], kSlack - mo[i]));
+          else if (whole || s[m][n][e] > -INFINITY) x = ex2(fmaf(raw_s[m][n][e], keep_f[i], ref[i]));
           else x = s[m][n][e] == -INFINITY ? 0.f : s[m][n][e];
           l[i] += x;
           w[e] = x * cv[i];

@@ -694,7 +694,7 @@ def test_calls_on_two_streams_do_not_share_scratch(many_heads):
                 assert torch.equal(x, y)
 
 
-def _one_hot(c, q, out, sc):
+def _one_hot(c, q, out, sc, win=None, ctx=None, tail=None):
     """Rows whose largest logit lies so far above the others, past what fp32 sums may be off by, that one token has all
     the weight: those outputs.  How many there are."""
     B, nq, HG, d = q.shape
@@ -704,6 +704,9 @@ def _one_hot(c, q, out, sc):
     half = q.dtype == torch.bfloat16
     for b, p, h, g in np.ndindex(B, nq, H, G):
         k, v = c.values["k"][b][h], c.values["v"][b][h]
+        if win:
+            see = max(0, tail[b] - (nq - 1 - p))
+            k, v = (np.concatenate([x, kv8.ring_rows(_f64(r[b]), ctx[b], tail[b])[:see, h]]) for x, r in zip((k, v), win))
         s = sc * (k @ q64[b, p, h, g])
         off = sc * (np.abs(k) @ np.abs(q64[b, p, h, g])).max() * (2.0 ** -21 + (d + 4) * 2.0 ** -23)
         top, second = np.sort(s)[::-1][:2]
@@ -786,3 +789,25 @@ def test_a_flat_rest_beside_a_peak_and_an_unattended_block(G, N, ratio):
     ref = a @ val
     bound = a @ val.abs() * 2.0 ** -10 + a[:, :1] * 1.27 * N * 2.0 ** -27 + ref.abs() * 2.0 ** -8
     assert ((out[0, 0].double().cpu() - ref).abs() <= bound).all()
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("wdt", [None, "bf16", "f32"])
+@pytest.mark.parametrize("G", [1, 5, 20])
+def test_huge_logits_give_their_token(G, wdt, io):
+    """As above in the kernel for few rows and among exact tokens; value scales from 2^-30 to 2^20."""
+    c = Cache(22, 2, 2, 64, 32, 320, "e4m3", [300, 20])
+    f = torch.tensor([2.0 ** e for e in (6, 20, -30, 5, 9, -12, 0, 3, -2, 1)], device="cuda")
+    c.v_scale *= f
+    c.values["v"] = [v * f.double().cpu().numpy()[np.arange(v.shape[1]) // 32][None, :, None] for v in c.values["v"]]
+    g = torch.Generator().manual_seed(2)
+    win = [_randn(g, 2, 128, 2, 64).to(IO[wdt]).cuda() for _ in range(2)] if wdt else None
+    ctx, tail = [500, 77], [128, 70]
+    for factor in HUGE:
+        q = (factor * torch.randn(2, 3, 2 * G, 64, generator=g)).to(IO[io]).cuda()
+        out = _run_attn(c, q, win, ctx, tail)
+        assert torch.isfinite(out).all()
+        assert _one_hot(c, q, out, 1 / 8, win, ctx, tail) >= 6 * G
+        w = torch.zeros(2, 2, 320, device="cuda")
+        _one_hot(c, q, _run_attn(c, q, win, ctx, tail, weights=w), 1 / 8, win, ctx, tail)
+        assert torch.isfinite(w).all() and w.min() >= 0
