@@ -406,7 +406,8 @@ typedef struct {
   lla_i32 len;             /* cached tokens, 0..Ncap: all seen by every query   */
   int32_t nq, G;           /* query positions (the last nq of the context) and
                               query heads per cache head (grouped heads, or the
-                              loops that share a per-head latent)               */
+                              loops that share a per-head latent); nq * G up to
+                              65535, H * G below 2^31                           */
   const void *q;           /* [B, nq, H * G, d]: head h reads cache head h / G;
                               post-rotary, or absorbed; inner [H * G, d] dense  */
   void *out;               /* as q, LLA_F32 or LLA_BF16; may not overlap inputs */

@@ -374,7 +374,7 @@ int check_kv8_attn(const lla_kv8_attn_params& p) {
   if (st != LLA_OK) return st;
   if (!dtype_ok(p.dtype) || (p.win_k && !dtype_ok(p.win_dtype))) return LLA_ERR_DTYPE;
   if (p.nq < 0 || p.G < 1) return LLA_ERR_SHAPE;
-  if ((int64_t)p.nq * p.G > 65535) return LLA_ERR_UNSUPPORTED;
+  if ((int64_t)p.nq * p.G > 65535 || (int64_t)p.cache.H * p.G > INT32_MAX) return LLA_ERR_UNSUPPORTED;   // 32-bit rows, heads
   if ((st = check_i32(p.len)) != LLA_OK) return st;
   if (!p.len.at && (p.len.all < 0 || p.len.all > p.cache.Ncap)) return LLA_ERR_SHAPE;
   if (!std::isfinite(p.scale) || p.scale < 0.f) return LLA_ERR_SHAPE;

@@ -275,3 +275,15 @@ def test_scratch_is_taken_on_the_stream_that_runs_the_call(monkeypatch):
         assert rec.taken.pop() == (512, torch.device("cuda", 0), stream)
         assert address == kept.data_ptr() and have == 512
     assert L._kv8_workspace(lambda p: 0, None, 0, None, side) == (None, 0, None) and not rec.taken
+
+
+def test_attn_refuses_more_query_heads_than_32_bits_number():
+    """Head h * G + g is a 32-bit number in the kernels: past it rows would lie outside the caller's buffers."""
+    for H, G, status in ((65535, 32768, 0), (65535, 32769, _abi.LLA_ERR_UNSUPPORTED)):
+        cache = dict(B=0, H=H)          # an empty batch: a call that is not refused does nothing
+        assert L.lib().lla_kv8_attn(ctypes.byref(_attn(cache, G=G)), None, 0, None) == status
+    row = 65535 * 65535 * 64
+    p = _attn(dict(H=65535, stride_b=65535 * 128 * 64, scale_stride_b=65535 * 4), G=65535, q_stride_b=row, q_stride_n=row,
+              out_stride_b=row, out_stride_n=row, weights_stride_b=65535 * 128)
+    assert L.lib().lla_kv8_attn_workspace_bytes(ctypes.byref(p)) == 0
+    assert L.lib().lla_kv8_attn(ctypes.byref(p), None, 0, None) == _abi.LLA_ERR_UNSUPPORTED
