@@ -418,7 +418,7 @@ typedef struct {
    * call is context position ctx - nq + p and sees those up to its own.
    * win_k NULL: none (ctx and tail are not read). */
   const void *win_k, *win_v;              /* [B, Wcap, H, d], d dense           */
-  int32_t win_dtype, Wcap;
+  int32_t win_dtype, Wcap;                /* Wcap 1..2^30                       */
   int64_t win_stride_b, win_stride_n, win_stride_h;
   lla_i32 ctx, tail;       /* tail 0..Wcap                                      */
   float scale;             /* 0 -> 1/sqrt(d)                                    */

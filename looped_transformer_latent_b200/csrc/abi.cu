@@ -388,6 +388,7 @@ int check_kv8_attn(const lla_kv8_attn_params& p) {
   if (p.q == p.out) return LLA_ERR_UNSUPPORTED;
   if (p.win_k) {
     if (p.Wcap < 1) return LLA_ERR_SHAPE;
+    if (p.Wcap > 1 << 30) return LLA_ERR_UNSUPPORTED;          // slots are summed in 32 bits
     if ((st = check_i32(p.ctx)) != LLA_OK || (st = check_i32(p.tail)) != LLA_OK) return st;
     if (!p.tail.at && (p.tail.all < 0 || p.tail.all > p.Wcap)) return LLA_ERR_SHAPE;
     if (!p.ctx.at && p.ctx.all < 0) return LLA_ERR_SHAPE;

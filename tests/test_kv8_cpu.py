@@ -287,3 +287,13 @@ def test_attn_refuses_more_query_heads_than_32_bits_number():
               out_stride_b=row, out_stride_n=row, weights_stride_b=65535 * 128)
     assert L.lib().lla_kv8_attn_workspace_bytes(ctypes.byref(p)) == 0
     assert L.lib().lla_kv8_attn(ctypes.byref(p), None, 0, None) == _abi.LLA_ERR_UNSUPPORTED
+
+
+def test_attn_refuses_rings_whose_slots_pass_32_bits():
+    """Slot of the oldest token plus a token's number, both below Wcap, is summed in 32 bits."""
+    lib = L.lib()
+    for wcap, status in ((1 << 30, _abi.LLA_ERR_WORKSPACE), ((1 << 30) + 1, _abi.LLA_ERR_UNSUPPORTED),
+                         ((1 << 31) - 1, _abi.LLA_ERR_UNSUPPORTED)):
+        p = _attn(Wcap=wcap, win_stride_b=0, win_stride_n=0, tail=_i32(at=20 * FAKE))
+        assert lib.lla_kv8_attn(ctypes.byref(p), None, 0, None) == status
+        assert (lib.lla_kv8_attn_workspace_bytes(ctypes.byref(p)) > 0) == (status == _abi.LLA_ERR_WORKSPACE)
