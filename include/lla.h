@@ -420,7 +420,8 @@ typedef struct {
   const void *win_k, *win_v;              /* [B, Wcap, H, d], d dense           */
   int32_t win_dtype, Wcap;                /* Wcap 1..2^30                       */
   int64_t win_stride_b, win_stride_n, win_stride_h;
-  lla_i32 ctx, tail;       /* tail 0..Wcap                                      */
+  lla_i32 ctx, tail;       /* ctx >= 0; tail 0..min(Wcap, ctx) (an `all` above
+                              ctx is clamped too)                               */
   float scale;             /* 0 -> 1/sqrt(d)                                    */
   /* Optional accumulator [B, H, Ncap] fp32 (NULL: none): the softmax weight of
    * each cached token, summed over the call's nq * G queries of its head, is

@@ -629,11 +629,12 @@ def lla_kv8_attn(*, q, k8, v8, k_scale, v_scale, lens, out, win_k=None, win_v=No
     q [B,nq,H*G,d] (float32 or bfloat16; head h reads cache head h // G), out
     likewise; cache as lla_kv8_write fills it, of which each query sees the
     first lens[b] tokens; ring win_k, win_v [B,Wcap,H,d] holds the last tail[b]
-    positions of a context of ctx[b] tokens, position j in row j mod Wcap, and
-    query p (context position ctx - nq + p) sees those up to its own.  lens,
-    ctx, tail: an int for all sequences or an int32 CUDA tensor [B].  weights
-    [B,H,Ncap] float32, optional: the softmax weights of the cached tokens are
-    added, summed over the queries of their head.  scale 0: 1/sqrt(d).
+    (at most ctx[b]) positions of a context of ctx[b] tokens, position j in row
+    j mod Wcap, and query p (context position ctx - nq + p) sees those up to
+    its own.  lens, ctx, tail: an int for all sequences or an int32 CUDA tensor
+    [B].  weights [B,H,Ncap] float32, optional: the softmax weights of the
+    cached tokens are added, summed over the queries of their head.  scale 0:
+    1/sqrt(d).
     """
     dev = _kv8_device(q, k8, v8, k_scale, v_scale, out, win_k, win_v, weights, lens, ctx, tail)
     p = _kv8_attn_params(q, k8, v8, k_scale, v_scale, lens, out, win_k, win_v, ctx, tail, scale, weights)

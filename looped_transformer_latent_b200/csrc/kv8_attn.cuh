@@ -468,10 +468,8 @@ __device__ __noinline__ void exact_split(const Kv8AttnArgs& a, Smem<D, NT, MT>& 
   const lla_kv8_attn_params& p = a.p;
   const int d = p.cache.d, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
   const Place at(a, RT);
-  const int tail = min(max(kv8_at(p.tail, at.b), 0), p.Wcap);
-  const int64_t pos0 = (int64_t)kv8_at(p.ctx, at.b) - tail;
-  int slot0 = (int)(pos0 % p.Wcap);              // of the oldest exact token
-  if (slot0 < 0) slot0 += p.Wcap;
+  const int ctx = max(kv8_at(p.ctx, at.b), 0), tail = min(max(kv8_at(p.tail, at.b), 0), min(p.Wcap, ctx));
+  const int slot0 = (ctx - tail) % p.Wcap;       // of the oldest exact token
   const int rows = min(RT, a.rows - at.row0);
   const int first = (at.split - a.S) * a.tpc;
   const int last = min(first + a.tpc, visible(tail, (a.row0 + at.row0 + rows - 1) / p.G, p.nq));

@@ -811,3 +811,23 @@ def test_huge_logits_give_their_token(G, wdt, io):
         w = torch.zeros(2, 2, 320, device="cuda")
         _one_hot(c, q, _run_attn(c, q, win, ctx, tail, weights=w), 1 / 8, win, ctx, tail)
         assert torch.isfinite(w).all() and w.min() >= 0
+
+
+@pytest.mark.parametrize("G", [2, 40])
+def test_a_tail_longer_than_the_context_is_the_context(G):
+    """A ring that is not full yet, read with tail = its size: slots that no position has reached hold NaN."""
+    c = Cache(5, 3, 2, 64, 32, 96, "i8", [70, 0, 33])
+    g = torch.Generator().manual_seed(1)
+    ctx = [5, 0, 16]
+    win = [torch.randn(3, 16, 2, 64, generator=g) for _ in range(2)]
+    for b in range(3):
+        for x in win:
+            x[b, ctx[b]:] = math.nan
+    win = [x.to(torch.bfloat16).cuda() for x in win]
+    q = torch.randn(3, 3, 2 * G, 64, generator=g).to(torch.bfloat16).cuda()
+    _check(c, q, _run_attn(c, q, win, ctx, [16, 16, 16]), win, ctx, ctx)
+    _check(c, q, _run_attn(c, q, win, [-4, -1, 2], [1, 0, 9]), win, [0, 0, 2], [0, 0, 2])
+    out = torch.zeros_like(q)
+    L.lla_kv8_attn(q=q, out=out, lens=_i32(c.lens), win_k=win[0], win_v=win[1], ctx=2, tail=16, **c.args())
+    again = _run_attn(c, q, win, [2, 2, 2], [2, 2, 2])
+    assert torch.equal(out[::2], again[::2])
