@@ -436,6 +436,8 @@ typedef struct {
  * Precision: codes are exact in the products; queries and probabilities enter
  * them as one f16 term for bf16 output, as two (about 22 bits) for fp32;
  * statistics and sums are fp32. */
+/* The size holds for the device that is current (its processor count decides
+ * on the splits), as does lla_kv8_evict_workspace_bytes; 0: ws is not used. */
 size_t lla_kv8_attn_workspace_bytes(const lla_kv8_attn_params *p);
 int lla_kv8_attn(const lla_kv8_attn_params *p, void *ws, size_t ws_bytes, lla_stream stream);
 

@@ -522,14 +522,18 @@ def _on(dev, fn, where, params, *mid, stream):
         raise LLAError(st, where)
 
 
-def _kv8_workspace(size, params, dev, workspace, stream):
-    """(address, bytes, tensor) of a call's scratch; sizes follow dev's processor count."""
+def _kv8_size(size, params, dev):
+    """Bytes of scratch on device number dev (its processor count decides on splits); negative: no device."""
     cuda = _torch().cuda
-    if dev == cuda.current_device():
-        need = size(params)
-    else:
-        with cuda.device(dev):
-            need = size(params)
+    if dev < 0 or dev == cuda.current_device():
+        return size(params)
+    with cuda.device(dev):
+        return size(params)
+
+
+def _kv8_workspace(size, params, dev, workspace, stream):
+    """(address, bytes, tensor) of a call's scratch."""
+    need = _kv8_size(size, params, dev)
     if need and workspace is None:
         workspace = _scratch(need, _torch().device("cuda", dev), stream)
     elif need and workspace.get_device() != dev:
@@ -619,7 +623,7 @@ def _kv8_weights(w, c):
 def lla_kv8_attn_workspace_bytes(**kw):
     kw.pop("workspace", None)
     kw.pop("stream", None)
-    return lib().lla_kv8_attn_workspace_bytes(_kv8_attn_params(**kw))
+    return _kv8_size(lib().lla_kv8_attn_workspace_bytes, _kv8_attn_params(**kw), kw["k8"].get_device())
 
 
 def lla_kv8_attn(*, q, k8, v8, k_scale, v_scale, lens, out, win_k=None, win_v=None, ctx=None, tail=0, scale=0.0,
@@ -665,7 +669,7 @@ def _kv8_evict_params(k8, v8, k_scale, v_scale, weights, lens, keep, first=0, la
 def lla_kv8_evict_workspace_bytes(**kw):
     kw.pop("workspace", None)
     kw.pop("stream", None)
-    return lib().lla_kv8_evict_workspace_bytes(_kv8_evict_params(**kw))
+    return _kv8_size(lib().lla_kv8_evict_workspace_bytes, _kv8_evict_params(**kw), kw["k8"].get_device())
 
 
 def lla_kv8_evict(*, k8, v8, k_scale, v_scale, weights, lens, keep, first=0, last=1, to=None, kept=None,

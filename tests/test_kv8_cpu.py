@@ -297,3 +297,21 @@ def test_attn_refuses_rings_whose_slots_pass_32_bits():
         p = _attn(Wcap=wcap, win_stride_b=0, win_stride_n=0, tail=_i32(at=20 * FAKE))
         assert lib.lla_kv8_attn(ctypes.byref(p), None, 0, None) == status
         assert (lib.lla_kv8_attn_workspace_bytes(ctypes.byref(p)) > 0) == (status == _abi.LLA_ERR_WORKSPACE)
+
+
+def test_workspace_sizes_are_those_of_the_tensors_device(monkeypatch):
+    rec, asked = _Recorder(monkeypatch), []
+
+    def size(p):
+        asked.append(rec.now["device"])
+        return 64
+
+    monkeypatch.setattr(L, "lib", lambda: type("Lib", (), {"lla_kv8_attn_workspace_bytes": staticmethod(size),
+                                                           "lla_kv8_evict_workspace_bytes": staticmethod(size)}))
+    k8, s, w = torch.zeros(1, 2, 32, 16, dtype=torch.int8), torch.zeros(1, 2, 2), torch.zeros(1, 2, 32)
+    q, lens = torch.zeros(1, 1, 2, 16), torch.zeros(1, dtype=torch.int32)
+    for dev in (0, 3):
+        monkeypatch.setattr(torch.Tensor, "get_device", lambda t, dev=dev: dev)
+        assert L.lla_kv8_attn_workspace_bytes(q=q, k8=k8, v8=k8, k_scale=s, v_scale=s, lens=32, out=q) == 64
+        assert L.lla_kv8_evict_workspace_bytes(k8=k8, v8=k8, k_scale=s, v_scale=s, weights=w, lens=lens, keep=1) == 64
+    assert asked == [0, 0, 3, 3] and rec.now["device"] == 0
