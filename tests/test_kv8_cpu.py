@@ -315,3 +315,23 @@ def test_workspace_sizes_are_those_of_the_tensors_device(monkeypatch):
         assert L.lla_kv8_attn_workspace_bytes(q=q, k8=k8, v8=k8, k_scale=s, v_scale=s, lens=32, out=q) == 64
         assert L.lla_kv8_evict_workspace_bytes(k8=k8, v8=k8, k_scale=s, v_scale=s, weights=w, lens=lens, keep=1) == 64
     assert asked == [0, 0, 3, 3] and rec.now["device"] == 0
+
+
+def test_axes_of_one_element_may_carry_any_stride():
+    """K from one buffer and V from another whose batch or head axis is longer: the same layout where it counts."""
+    def pair(shape, dtype=torch.float32):
+        long = torch.zeros(shape[0] * 3, *shape[1:], dtype=dtype)
+        return torch.zeros(*shape, dtype=dtype), long.as_strided(shape, (7 * long.stride(0), *long.stride()[1:]))
+
+    k8, v8 = pair((1, 2, 32, 16), torch.int8)
+    ks, vs = pair((1, 2, 2))
+    wk, wv = pair((1, 8, 2, 16))
+    assert k8.stride() != v8.stride() and ks.stride() != vs.stride() and wk.stride() != wv.stride()
+    q = torch.zeros(1, 1, 2, 16)
+    args = dict(q=q, k8=k8, v8=v8, k_scale=ks, v_scale=vs, lens=32, out=q.clone(), win_k=wk, win_v=wv, ctx=3, tail=3)
+    p = L._kv8_attn_params(**args)
+    assert (p.cache.stride_h, p.win_stride_n, p.cache.scale_stride_h) == (32 * 16, 32, 2)
+    with pytest.raises(ValueError):
+        L._kv8_attn_params(**{**args, "v8": torch.zeros(1, 32, 2, 16, dtype=torch.int8).transpose(1, 2)})
+    with pytest.raises(ValueError):
+        L._kv8_attn_params(**{**args, "win_v": torch.zeros(1, 2, 8, 16).transpose(1, 2)})
