@@ -136,6 +136,8 @@ def _workspace(nbytes, device, workspace, stream):
         return None, 0, None
     if workspace is None:
         workspace = _scratch(nbytes, device, stream)
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
     if workspace.numel() * workspace.element_size() < nbytes:
         raise ValueError(f"workspace too small: {workspace.numel()} < {nbytes} bytes")
     return ctypes.c_void_p(workspace.data_ptr()), workspace.numel() * workspace.element_size(), workspace
@@ -544,6 +546,8 @@ def _kv8_workspace(size, params, dev, workspace, stream):
         workspace = _scratch(need, _torch().device("cuda", dev), stream)
     elif need and workspace.get_device() != dev:
         raise ValueError("workspace is on another device")
+    elif need and not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
     if not need:
         return None, 0, None
     have = workspace.numel() * workspace.element_size()

@@ -335,3 +335,17 @@ def test_axes_of_one_element_may_carry_any_stride():
         L._kv8_attn_params(**{**args, "v8": torch.zeros(1, 32, 2, 16, dtype=torch.int8).transpose(1, 2)})
     with pytest.raises(ValueError):
         L._kv8_attn_params(**{**args, "win_v": torch.zeros(1, 2, 8, 16).transpose(1, 2)})
+
+
+def test_workspace_views_with_gaps_or_shared_bytes_are_refused(monkeypatch):
+    """Their element count says nothing about the bytes behind their address."""
+    rec = _Recorder(monkeypatch)
+    monkeypatch.setattr(torch.Tensor, "get_device", lambda t: rec.now["device"])
+    for ws in (torch.zeros(1, dtype=torch.uint8).expand(4096), torch.zeros(8192, dtype=torch.uint8)[::2]):
+        with pytest.raises(ValueError, match="contiguous"):
+            L._kv8_workspace(lambda p: 512, None, 0, ws, None)
+        with pytest.raises(ValueError, match="contiguous"):
+            L._workspace(512, torch.device("cuda", 0), ws, None)
+    ws = torch.zeros(64, 64, dtype=torch.uint8)
+    assert L._kv8_workspace(lambda p: 512, None, 0, ws, None)[:2] == (ws.data_ptr(), 4096)
+    assert L._workspace(512, torch.device("cuda", 0), ws, None)[1] == 4096
