@@ -685,8 +685,8 @@ def lla_kv8_evict(*, k8, v8, k_scale, v_scale, weights, lens, keep, first=0, las
                   workspace=None, stream=None):
     """Keep the `keep` blocks of each head that gathered the most weight.
 
-    Cache and weights [B,H,Ncap] as lla_kv8_attn reads and adds them; lens int32
-    [B].  Of a sequence of more than `keep` blocks the first `first`, the last
+    Cache (at most 8192 blocks a head) and weights [B,H,Ncap] as lla_kv8_attn
+    reads and adds them; lens int32 [B].  Of a sequence of more than `keep` blocks the first `first`, the last
     `last` (>= 1) and, of the others, those whose tokens' weights sum highest
     stay, in order, moved to the front.  In place, or into `to`: a dict of k8,
     v8, k_scale, v_scale, weights and lens of another cache (which may have

@@ -831,3 +831,29 @@ def test_a_tail_longer_than_the_context_is_the_context(G):
     L.lla_kv8_attn(q=q, out=out, lens=_i32(c.lens), win_k=win[0], win_v=win[1], ctx=2, tail=16, **c.args())
     again = _run_attn(c, q, win, [2, 2, 2], [2, 2, 2])
     assert torch.equal(out[::2], again[::2])
+
+
+@pytest.mark.parametrize("H,keep", [(1, 8192), (1, 8191), (2, 6000), (149, 5), (149, 8000)])
+def test_eviction_of_the_most_blocks(H, keep):
+    """8192 blocks: keys and the list of kept blocks fill the most shared memory, with few heads and with many."""
+    B, d, block, cap = 1, 16, 16, 8192 * 16
+    g = torch.Generator(device="cuda").manual_seed(keep)
+    n = cap - 5
+    k8, v8 = (torch.randint(-127, 128, (B, H, cap, d), generator=g, device="cuda", dtype=torch.int8) for _ in range(2))
+    ks, vs = (torch.rand(B, H, cap // block, generator=g, device="cuda") for _ in range(2))
+    w = torch.randint(0, 50, (B, H, cap), generator=g, device="cuda").float()     # sums are exact, and many are equal
+    lens, kept = _i32([n]), torch.empty(B, H, keep, dtype=torch.int32, device="cuda")
+    was = [t.clone() for t in (k8, v8, ks, vs, w)]
+    L.lla_kv8_evict(k8=k8, v8=v8, k_scale=ks, v_scale=vs, weights=w, lens=lens, keep=keep, first=2, last=2, kept=kept)
+    new = n - (8192 - keep) * block
+    assert lens.tolist() == [new]
+    mass = was[4].view(H, -1, block).sum(-1)
+    mass[:, :2] = mass[:, -2:] = math.inf
+    ids = mass.sort(dim=-1, descending=True, stable=True).indices[:, :keep].sort(-1).values
+    assert torch.equal(kept[0].long(), ids)
+    rows = (ids[..., None] * block + torch.arange(block, device="cuda")).flatten(1)[:, :new]
+    for x, y in ((k8, was[0]), (v8, was[1])):
+        assert torch.equal(x[0, :, :new], y[0].gather(1, rows[..., None].expand(-1, -1, d)))
+    for x, y in ((ks, was[2]), (vs, was[3])):
+        assert torch.equal(x[0, :, :keep], y[0].gather(1, ids))
+    assert torch.equal(w[0, :, :new], was[4][0].gather(1, rows)) and not w[0, :, new:n].any()
