@@ -442,7 +442,8 @@ size_t lla_kv8_attn_workspace_bytes(const lla_kv8_attn_params *p);
 int lla_kv8_attn(const lla_kv8_attn_params *p, void *ws, size_t ws_bytes, lla_stream stream);
 
 typedef struct {
-  lla_kv8_cache src, dst;  /* same B, H, d, block, code; dst either is src (same
+  lla_kv8_cache src, dst;  /* same B, H, d, block, code; src of at most 8192
+                              blocks (Ncap / block); dst either is src (same
                               pointers and strides: in place) or overlaps
                               neither it nor its weights                        */
   const float *weights;    /* [B, H, src.Ncap], as lla_kv8_attn adds them up    */
@@ -450,7 +451,8 @@ typedef struct {
   float *dst_weights;      /* [B, H, dst.Ncap]; `weights` itself in place       */
   int64_t dst_weights_stride_b, dst_weights_stride_h;
   const int32_t *len;      /* device [B]: tokens of each sequence, 0..src.Ncap  */
-  int32_t *dst_len;        /* device [B], written; may be `len` itself          */
+  int32_t *dst_len;        /* device [B], written; may be `len` itself, and
+                              overlaps it no other way                          */
   int32_t keep;            /* blocks kept per head, <= src.Ncap / block and
                               <= dst.Ncap / block                               */
   int32_t first, last;     /* of these, the first and the last blocks that are

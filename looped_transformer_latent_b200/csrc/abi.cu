@@ -493,6 +493,9 @@ int check_kv8_evict(const lla_kv8_evict_params& p) {
       (p.kept && !aligned(p.kept, 4)))
     return LLA_ERR_ALIGN;
   if (p.weights_stride_b < 0 || p.weights_stride_h < 0) return LLA_ERR_SHAPE;
+  // a sequence's new length must not take the place of another's old one while that is read
+  const intptr_t gap = reinterpret_cast<intptr_t>(p.dst_len) - reinterpret_cast<intptr_t>(p.len);
+  if (gap != 0 && gap < 4 * (intptr_t)p.src.B && -gap < 4 * (intptr_t)p.src.B) return LLA_ERR_UNSUPPORTED;
   if (!cache_apart(p.dst) ||
       !apart(p.dst.B, p.dst_weights_stride_b, p.dst.H, p.dst_weights_stride_h, p.dst.Ncap))
     return LLA_ERR_SHAPE;

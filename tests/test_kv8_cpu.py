@@ -349,3 +349,10 @@ def test_workspace_views_with_gaps_or_shared_bytes_are_refused(monkeypatch):
     ws = torch.zeros(64, 64, dtype=torch.uint8)
     assert L._kv8_workspace(lambda p: 512, None, 0, ws, None)[:2] == (ws.data_ptr(), 4096)
     assert L._workspace(512, torch.device("cuda", 0), ws, None)[1] == 4096
+
+
+@pytest.mark.parametrize("gap,status", [(4, "UNSUPPORTED"), (-4, "UNSUPPORTED"), (0, "SHAPE"), (8, "SHAPE"), (-8, "SHAPE")])
+def test_evict_refuses_lengths_that_overlap_in_part(gap, status):
+    # two sequences; the calls that this check lets pass are refused by a later one
+    p = _evict(len=13 * FAKE, dst_len=13 * FAKE + gap, dst_weights_stride_h=127)
+    assert L.lib().lla_kv8_evict(ctypes.byref(p), None, 0, None) == getattr(_abi, "LLA_ERR_" + status)
