@@ -952,10 +952,13 @@ __device__ __forceinline__ void cached_split(const Kv8AttnArgs& a, Smem<D, NT, M
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const int i = 2 * n + e;
-      m[i] = mo[i] > kUnset ? (QT == 1 ? mo[i] : mo[i] - kSlack) : -INFINITY;
+      m[i] = mo[i] > kUnset ? mo[i] : -INFINITY;
 #pragma unroll
       for (int o = 4; o < 32; o <<= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], o);
-      const float unit = 1.f / F[i];
+      // QT 2 summed p 2^kSlack; a power of two less here, as m less kSlack is m again where logits are huge
+      const float less = QT == 1 ? 1.f : 0x1p-12f, unit = less / F[i];
+      static_assert(kSlack == 12.f, "its power of two");
+      l[i] *= less;
 #pragma unroll
       for (int k = 0; k < D / 16; ++k) { acc[k][n][e] *= unit; acc[k][n][e + 2] *= unit; }
     }

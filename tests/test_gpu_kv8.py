@@ -857,3 +857,42 @@ def test_eviction_of_the_most_blocks(H, keep):
     for x, y in ((ks, was[2]), (vs, was[3])):
         assert torch.equal(x[0, :, :keep], y[0].gather(1, ids))
     assert torch.equal(w[0, :, :new], was[4][0].gather(1, rows)) and not w[0, :, new:n].any()
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("G", [1, 5, 20, 40])
+def test_weights_of_huge_logits_sum_to_the_rows(G, io):
+    """A weight is formed from a kept score and the joined statistics, which must stand in the same units."""
+    c = Cache(22, 2, 2, 64, 32, 320, "i8", [300, 20])
+    g = torch.Generator().manual_seed(2)
+    for factor in HUGE:
+        q = (factor * torch.randn(2, 2, 2 * G, 64, generator=g)).to(IO[io]).cuda()
+        w = torch.zeros(2, 2, 320, device="cuda")
+        _run_attn(c, q, weights=w)
+        # past 2^24 a logit's rounding is worth a bit and more: then only rows of one token say what a weight is
+        off = factor * 40 * 2.0 ** -22 if factor < 2.0 ** 14 else 2.0 ** -16
+        top, got = _tops(c, q), _f64(w)
+        for b, h in np.ndindex(2, 2):
+            sure = top[b][h] >= 0
+            if sure.all():
+                want = np.bincount(top[b][h], minlength=320)
+                assert np.all(np.abs(got[b, h] - want) <= off * np.maximum(want, 1) + 2.0 ** -20)
+        assert factor < 2.0 ** 14 or (top[1][0] >= 0).all()
+
+
+def _tops(c, q):
+    """[b][h]: for each row the token that has all its weight, -1 where none has beyond what fp32 sums may be off by."""
+    B, nq, HG, d = q.shape
+    H = c.k8.shape[1]
+    q64 = _f64(q).reshape(B, nq, H, HG // H, d)
+    out = []
+    for b in range(B):
+        per = []
+        for h in range(H):
+            k, r = c.values["k"][b][h], q64[b, :, h].reshape(-1, d)
+            s = r @ k.T / math.sqrt(d)
+            off = (np.abs(r) @ np.abs(k).T).max(1) / math.sqrt(d) * (2.0 ** -21 + (d + 4) * 2.0 ** -23)
+            two = np.sort(s, 1)[:, -2:]
+            per.append(np.where(two[:, 1] - two[:, 0] > 2 * off + 60, s.argmax(1), -1))
+        out.append(per)
+    return out
