@@ -345,7 +345,9 @@ int hla_decode_attn_noalloc(const hla_decode_params *p, lla_stream stream);
 /* A cache of exact K/V vectors of one loop and layer, or of per-head latents
  * (LLA abstract, per-head codec), held in 8 bits: for each head one code per
  * element, and one fp32 scale per part (K, V) for each block of `block`
- * tokens.  The stored value of an element is code * scale.  The HLA summary
+ * tokens.  Latents are read absorbed, by themselves: exact tokens beside a cache
+ * have its width, and no call returns a row's maximum and sum, so a read of
+ * latents cannot be joined with exact tokens of another width.  The stored value of an element is code * scale.  The HLA summary
  * names quantisation and token eviction as what latent caches combine with
  * ("Conclusion / Future directions"); the format is this library's:
  *   s = amax / top over the block's tokens and the head's d elements (top =
@@ -415,7 +417,9 @@ typedef struct {
   int64_t q_stride_b, q_stride_n, out_stride_b, out_stride_n;
   /* Exact tokens after the cached ones: the last `tail` positions of a context
    * of ctx tokens, position j in ring slot j mod Wcap.  Query position p of the
-   * call is context position ctx - nq + p and sees those up to its own.
+   * call is context position ctx - nq + p and sees those up to its own.  An
+   * infinity or a NaN in one reaches no outputs but those of the queries that see
+   * it, which it may turn into infinities and NaN.
    * win_k NULL: none (ctx and tail are not read). */
   const void *win_k, *win_v;              /* [B, Wcap, H, d], d dense           */
   int32_t win_dtype, Wcap;                /* Wcap 1..2^30                       */
@@ -433,9 +437,12 @@ typedef struct {
 
 /* o = sum_j a_j v_j, a = softmax(scale * q . k_j) over the cached tokens and
  * the visible exact ones jointly.  A query that sees no token gives zeros.
- * Precision: codes are exact in the products; queries and probabilities enter
- * them as one f16 term for bf16 output, as two (about 22 bits) for fp32;
- * statistics and sums are fp32. */
+ * Precision: codes are exact in the products; queries (under a power of two of
+ * their row) and probabilities (under one of their row's largest contribution)
+ * enter them as one f16 term for bf16 output, as two (about 22 bits) for fp32;
+ * statistics and sums are fp32.  No row's output depends on another row's query.
+ * With weights the workspace holds the scores of a pass, 4 B H Ncap bytes for a
+ * row: of up to 32 rows, or of as many more as 256 MB hold. */
 /* The size holds for the device that is current (its processor count decides
  * on the splits), as does lla_kv8_evict_workspace_bytes; 0: ws is not used. */
 size_t lla_kv8_attn_workspace_bytes(const lla_kv8_attn_params *p);

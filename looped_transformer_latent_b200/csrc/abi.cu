@@ -411,8 +411,11 @@ struct Kv8AttnPlan {
 // time is least by this count: the CTAs that the fullest SM gets share its
 // bandwidth, one wave takes at least half of what its CTAs would take in turn,
 // and a CTA costs some tokens' worth besides its own.  Never below 128 tokens
-// (a step or two of each warp).  With weights the scores of a pass
-// are kept; more rows than fit kScoreBytes go in several passes.
+// (a step or two of each warp).  With lengths on the device the splits are planned
+// for Ncap tokens, and a shorter sequence leaves its last ones empty.  With weights
+// the scores of a pass are kept, 4 bytes for each row and token; more than 32 rows
+// go in several passes of 32 k rows when their scores exceed kScoreBytes.  Fewer
+// rows to a pass would read the cache more often, so 32 rows' scores may exceed it.
 constexpr size_t kScoreBytes = (size_t)256 << 20;
 
 Kv8AttnPlan plan_kv8_attn(const lla_kv8_attn_params& p) {
@@ -425,13 +428,14 @@ Kv8AttnPlan plan_kv8_attn(const lla_kv8_attn_params& p) {
     const int64_t fit = (int64_t)(kScoreBytes / sizeof(float)) / (bh * c.Ncap) / 32 * 32;
     pl.rows_pass = (int)std::min<int64_t>(pl.rows_pass, std::max<int64_t>(fit, 32));
   }
-  // 32 rows of more than 128 elements, or with two terms of each, do not fit a thread's registers.  fp32: two and three
-  // tiles of 8 rows take 55 and 82 us (64 heads of 96, up to 8000 tokens) where tiles of 16 take 84 and 94.  bf16, 512
-  // heads of 96, 4096 tokens: 16 rows 64 us in a tile of 16, 72 in two of 8.
+  // 32 rows of more than 128 elements, or with two terms of each, do not fit a thread's registers.  fp32, in tiles of 8
+  // and of 16 rows: 24 rows 76 and 107 us (64 heads of 96, up to 8000 tokens), 186 and 213 (256 heads of 128, 4096
+  // tokens); 16 rows 59 and 68 in the first, but 129 and 104 in the second.  bf16, 16 rows in a tile of 16 and in two of
+  // 8: 64 and 82 us (256 heads of 96, 4096 tokens), 121 and 135 (512 heads).
   const bool f32 = p.dtype == LLA_F32;
   pl.nt = pl.rows_pass <= (f32 ? 24 : 8) ? 1 : pl.rows_pass <= 16 || c.d > 128 || c.block < 32 || f32 ? 2 : 4;
   // 33 rows and more (bf16, d <= 128): the tcgen05 kernel.  256 heads, 4096 tokens, e4m3 of 128 / int8 of 96: 32 rows
-  // 138 / 139 us there and 86 / 82 in the mma.sync kernel, 48 rows 143 / 144 and 187 / 177, 128 rows 198 / 197 and 293 / 277.
+  // 143 / 143 us there and 90 / 86 in the mma.sync kernel, 48 rows 149 / 147 and 192 / 184, 128 rows 205 / 203 and 297 / 283.
   pl.wide = f32 || c.d > 128 || pl.rows_pass <= 32 ? 0 : pl.rows_pass <= 64 ? 64 : 128;
   const int tiles = ceil_div(pl.rows_pass, pl.wide ? pl.wide : 8 * pl.nt);
   pl.S = 0; pl.tps = 0;

@@ -21,7 +21,8 @@ namespace lla {
 // griddep_wait() before its first global-memory access (it returns once the
 // previous grid has completed and its writes are visible; without the
 // attribute it returns at once) and griddep_launch() as the last instruction
-// of its CTAs, after any TMEM is freed: dependents start only once every CTA
+// of its CTAs, after any TMEM is freed (the 8-bit cache's kernels leave it to
+// their exit, which does the same): dependents start only once every CTA
 // of this grid has started and finished its work, so no CTA of this grid ever
 // waits for resources held by a dependent.  Off by default: on the decode
 // steps measured it changed the step time by less than the run-to-run spread.

@@ -17,14 +17,17 @@
 // CTAs past the cached splits serve the exact tokens, with bf16 products of as
 // many terms as the types need.
 // Up to 8 rows it is bound by HBM: 32 x 16 heads of 128, 4096 e4m3 tokens and 129
-// exact ones take 108 us, 5.3 TB/s, 82 % of the copy rate; widened by shifts and
+// exact ones take 108 us, 5.3 TB/s, 81 % of the copy rate; widened by shifts and
 // masks instead of the conversion instruction the same read took 196.  Beyond, by
-// instruction issue: of 1.9 instructions a cycle with 32 rows, a quarter are
-// products (33 % of the pipe), a quarter the softmax, a fifth the widening; 16 x
-// 55 heads of 96, 32 rows, 4096 int8 tokens take 235 us (3.0 TB/s).  fp32 queries
-// double the products and add their sums apart: 300 MB of 96-element heads in 94
-// us.  Rings and not register prefetch: with 8 warps an SM the registers held
-// 24 KB under way, half of what the memory's latency asks for (462 us).
+// the latency of instructions that wait for one another: with 32 rows a thread
+// needs 255 registers, which leaves 8 warps an SM, and these issue 1.9 of 4
+// instructions a cycle (545 for 16 tokens, 48 of them products, 33 % of their
+// pipe); 16 x 55 heads of 96, 32 rows, 4096 int8 tokens take 235 us (3.0 TB/s).
+// fp32 queries double the products and add their sums apart: 585 instructions for
+// 16 tokens of one tile of 8 rows, 2.2 a cycle from 15 warps an SM, 300 MB of
+// 96-element heads with their weights in 99 us.  Rings and not register prefetch:
+// with 8 warps an SM the registers held 24 KB under way, half of what the memory's
+// latency asks for (462 us).
 #pragma once
 
 #include "kernels.cuh"

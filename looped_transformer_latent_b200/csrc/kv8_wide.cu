@@ -15,12 +15,15 @@
 // A row's reference is set kSlack above a new maximum; a tile whose logits pass
 // it is done again under a new one, twice at most, and the row's accumulators
 // are rescaled.
-// Bound by shared memory and the softmax: a tile writes 64 KB of widened codes
-// and 32 KB of P and the products read 128 KB, 1800 cycles at 128 bytes each,
-// and 128 rows' exponentials take 1024.  256 heads of 128, 4096 e4m3 tokens: 48
-// rows 143 us, 128 rows 198 (348 TFLOP/s).  A softmax thread for each token instead of
-// each row (and rows walked in registers) took 170 and 270: it votes on every
-// tile and its sums do not fit registers.
+// Bound by the chain from tile to tile, 5800 cycles each with 128 rows: K and V
+// have one f16 stage each that the same four warps fill, K of a tile after V of
+// the tile before, which waits for that stage's products, and these for the
+// softmax (39 % of the issue slots are used, the tensor pipe 18 % of the time).
+// Shared memory alone would take 1800 cycles (64 KB of widened codes and 32 KB of
+// P written, 128 KB read by the products), the exponentials 1024.  256 heads of 128,
+// 4096 e4m3 tokens: 48 rows 149 us, 128 rows 205 (335 TFLOP/s).  A softmax thread
+// for each token instead of each row (and rows walked in registers) took 170 and
+// 270: it votes on every tile and its sums do not fit registers.
 // Every wait is bounded; a CTA that gives up writes NaN.
 #include <type_traits>
 
