@@ -210,14 +210,20 @@ __device__ __forceinline__ void read_row(uint32_t* w, uint32_t base, int r, int 
 // next 11 bits of an fp32 one.
 constexpr int kQExp = 13;
 // Running references of a row, both base-2 exponents: m of the probabilities
-// p = exp2(s - m), a of what meets the value codes, w = 2^12 exp2(s + log2(scale) - a),
+// p = exp2(s - m), a of what meets the value codes, w = 2^kMost exp2(s + log2(scale) - a),
 // so that a block whose values are 2^60 times another's does not drown it.  A
 // reference is set kSlack above a new maximum and moves only when a logit
-// exceeds it: p <= 1, w <= 2^12 in f16 and the largest of them above 2^-1, and
-// most tiles need neither a shuffle nor a rescaling.  References are whole
+// exceeds it: p <= 1, w <= 2^15 in f16 and the largest of them above 2^2, and
+// most tiles need neither a shuffle nor a rescaling.  One f16 term loses what lies
+// 27 bits below the largest.  fp32: the second term is what the first leaves of w,
+// times kLow, and meets the codes first; its products are taken back by that
+// power of two, and what is lost lies 39 bits below the largest (without it a flat
+// rest of 4096 tokens of a warp, 25 bits below a peak, was lost: 1e-4 of the output).
+// References are whole
 // numbers, so that moving one is exact, and of a only m - a is kept, which means
 // the same however large the logits are.
-constexpr float kSlack = 12.f, kUnset = -3.4e38f;
+constexpr float kSlack = 12.f, kMost = 15.f, kUnset = -3.4e38f;
+constexpr float kLow = 0x1p12f, kLowInv = 0x1p-12f;
 // from here on the rounding of a product exceeds the slack of f16, and the difference to a reference is taken from
 // the rounded logit, which lies below it
 constexpr float kHuge = 16777216.f;
@@ -729,7 +735,7 @@ __device__ __forceinline__ void cached_split(const Kv8AttnArgs& a, Smem<D, NT, M
   __syncthreads();
 
   float acc[D / 16][NT][4];
-  float mo[2 * NT], da[2 * NT], F[2 * NT], l[2 * NT];   // reference m, m - a, F = 2^12 exp2(m - a), sums
+  float mo[2 * NT], da[2 * NT], F[2 * NT], l[2 * NT];   // reference m, m - a, F = 2^kMost exp2(m - a), sums
   bool huge = false;                                    // the warp has seen an |m| >= kHuge
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
@@ -860,12 +866,12 @@ __device__ __forceinline__ void cached_split(const Kv8AttnArgs& a, Smem<D, NT, M
           const bool over = top > mo[i];
           const float m1 = over ? ceilf(top) + kSlack : mo[i], up = over ? m1 - mo[i] : 0.f;
           const float a0 = -da[i] - up, v = top - m1 + lv;     // a, and the tile's largest s + log2(scale), less m1
-          // F vs stays below 2^100 and F below 2^112: blocks of tiny values lie at most 2^100 below
+          // F vs stays below 2^100 and F below 2^115: blocks of tiny values lie at most 2^100 below
           const float a1 = fmaxf(v > a0 ? ceilf(v) + kSlack : a0, fmaxf(-100.f, ceilf(lv) - 80.f));
           mo[i] = m1;
           da[i] = -a1;
           huge |= QT == 2 && fabsf(m1) >= kHuge;
-          F[i] = ex2(QT == 1 ? kSlack - a1 : -a1);
+          F[i] = ex2(QT == 1 ? kMost - a1 : kMost - kSlack - a1);
           cv[i] = vs * F[i];
           l[i] *= ex2(-up);
           const float r = ex2(a0 - a1);
@@ -914,7 +920,7 @@ __device__ __forceinline__ void cached_split(const Kv8AttnArgs& a, Smem<D, NT, M
           p0[n][i] = transpose8(hi);
           if (QT == 2) {
             const float2 u = unpack_f16(hi);
-            p1[n][i] = transpose8(pack_f16(w[2 * i] - u.x, w[2 * i + 1] - u.y));
+            p1[n][i] = transpose8(pack_f16((w[2 * i] - u.x) * kLow, (w[2 * i + 1] - u.y) * kLow));
           }
         }
       }
@@ -937,6 +943,8 @@ __device__ __forceinline__ void cached_split(const Kv8AttnArgs& a, Smem<D, NT, M
               // as above
               float y[4] = {0.f, 0.f, 0.f, 0.f};
               mma_f16(y, op, p1[n][0], p1[n][1]);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) y[i] *= kLowInv;
               mma_f16(y, op, p0[n][0], p0[n][1]);
 #pragma unroll
               for (int i = 0; i < 4; ++i) acc[2 * w + e][n][i] += y[i];

@@ -896,3 +896,31 @@ def _tops(c, q):
             per.append(np.where(two[:, 1] - two[:, 0] > 2 * off + 60, s.argmax(1), -1))
         out.append(per)
     return out
+
+
+@pytest.mark.parametrize("bits", [22, 24, 25, 26, 28])
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+def test_a_flat_rest_far_below_a_peak(io, bits):
+    """600 heads, so that one CTA sums a whole head and each warp a quarter: a peak and 65536 tokens `bits` below it, of
+    values that the peak does not have.  One f16 term may lose 2^-25 under a largest of 2^2 of each, two a 2^-37."""
+    H, N, d, block = 600, 65536, 64, 256
+    g = torch.Generator().manual_seed(bits)
+    k = torch.zeros(N, d, dtype=torch.int8)
+    k[100, 0] = 100
+    v = torch.randint(0, 128, (N, d), generator=g, dtype=torch.int8)
+    v[:, 32:] = 100
+    v[100, :32] = 0
+    q = torch.zeros(1, 1, H, d, device="cuda")
+    q[..., 0] = bits * math.log(2) * 8 / 100
+    q = q.to(IO[io])
+    out = torch.zeros_like(q)
+    k8, v8 = (x[None, None].cuda().expand(1, H, N, d) for x in (k, v))      # all heads read the same rows
+    ks, s = (torch.full((1, 1, N // block), x, device="cuda").expand(1, H, -1) for x in (1.0, 0.01))
+    L.lla_kv8_attn(q=q, out=out, lens=N, k8=k8, v8=v8, k_scale=ks, v_scale=s)
+    a = torch.softmax(float(q[0, 0, 0, 0]) * k[:, 0].double() / 8, 0)
+    ref = a @ (v.double() * float(s[0, 0, 0]))
+    # the weights: a logit of up to 28 bits, its product, sum and difference rounded, and sums of 65536 / 4 / 32 terms
+    rel = 28 * 2.0 ** -22 + 2.0 ** -20 + 2048 * 2.0 ** -24 / 8
+    lost = a.max().item() * 1.27 * N / 4 * (2.0 ** -27 if io == "bf16" else 2.0 ** -39)
+    tol = ref * (rel + (2.0 ** -10 + 2.0 ** -8 if io == "bf16" else 0)) + lost
+    assert ((out[0, 0].double().cpu() - ref).abs() <= tol).all()
