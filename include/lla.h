@@ -440,7 +440,8 @@ typedef struct {
  * Precision: codes are exact in the products; queries (under a power of two of
  * their row) and probabilities (under one of their row's largest contribution)
  * enter them as one f16 term for bf16 output, as two (about 22 bits) for fp32;
- * statistics and sums are fp32.  No row's output depends on another row's query.
+ * statistics and sums are fp32.  Contributions below 2^-70 of the largest cached
+ * value lose their bits.  No row's output depends on another row's query.
  * With weights the workspace holds the scores of a pass, 4 B H Ncap bytes for a
  * row: of up to 32 rows, or of as many more as 256 MB hold. */
 /* The size holds for the device that is current (its processor count decides
