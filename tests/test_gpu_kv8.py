@@ -924,3 +924,27 @@ def test_a_flat_rest_far_below_a_peak(io, bits):
     lost = a.max().item() * 1.27 * N / 4 * (2.0 ** -27 if io == "bf16" else 2.0 ** -39)
     tol = ref * (rel + (2.0 ** -10 + 2.0 ** -8 if io == "bf16" else 0)) + lost
     assert ((out[0, 0].double().cpu() - ref).abs() <= tol).all()
+
+
+def test_calls_on_forked_streams_of_one_capture():
+    """Scratch of the call on the forked stream comes from the capture's memory and is not the other call's."""
+    case = (3, 2, 2, 5, 64, 32, [900, 40, 640], "i8", "bf16", 16, [5, 9, 16], "bf16")
+    sets = [_inputs(case, seed) for seed in (0, 50)]
+    outs, before = [torch.zeros_like(s[1]) for s in sets], [s[5].clone() for s in sets]
+    side = torch.cuda.Stream()
+    args = [dict(q=q, out=o, lens=_i32(c.lens), win_k=win[0], win_v=win[1], ctx=_i32(ctx), tail=_i32(tails), weights=w,
+                 **c.args()) for (c, q, win, ctx, tails, w), o in zip(sets, outs)]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        main = torch.cuda.current_stream()
+        side.wait_stream(main)
+        L.lla_kv8_attn(**args[0])
+        L.lla_kv8_attn(stream=side, **args[1])
+        main.wait_stream(side)
+    for _ in range(3):
+        for (_, _, _, _, _, w), b in zip(sets, before):
+            w.copy_(b)
+        graph.replay()
+        torch.cuda.synchronize()
+        for (c, q, win, ctx, tails, w), o, b in zip(sets, outs, before):
+            _check(c, q, o, win, ctx, tails, w, b)
