@@ -431,7 +431,7 @@ __device__ __forceinline__ void load_quad(uint32_t (&o)[WT][2], const void* x, i
     for (int i = 0; i < WT; ++i) { o[i][0] = u[i]; o[i][1] = w[i]; }
   }
 }
-// Whether one of 4 elements is an infinity or a NaN.
+// Whether one of 4 elements is an infinity or a NaN, or becomes one as a bf16 term.
 template <int WT>
 __device__ __forceinline__ bool no_number(const void* x, int64_t at) {
   if constexpr (WT == 1) {
@@ -441,7 +441,7 @@ __device__ __forceinline__ bool no_number(const void* x, int64_t at) {
   } else {
     const uint4 v = __ldg(reinterpret_cast<const uint4*>(static_cast<const float*>(x) + at));
     const uint32_t m = 0x7fffffffu;
-    return max(max(v.x & m, v.y & m), max(v.z & m, v.w & m)) >= 0x7f800000u;
+    return max(max(v.x & m, v.y & m), max(v.z & m, v.w & m)) >= 0x7f7f8000u;
   }
 }
 

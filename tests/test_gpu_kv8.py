@@ -948,3 +948,29 @@ def test_calls_on_forked_streams_of_one_capture():
         torch.cuda.synchronize()
         for (c, q, win, ctx, tails, w), o, b in zip(sets, outs, before):
             _check(c, q, o, win, ctx, tails, w, b)
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("G", [1, 40])
+def test_values_near_the_largest_fp32_number(G, io):
+    """An fp32 ring's value that bf16 terms cannot hold: kept out of the queries that do not see it, and met as it is by
+    those that do."""
+    c = Cache(3, 1, 2, 64, 32, 96, "i8", [70])
+    g = torch.Generator().manual_seed(1)
+    q = torch.randn(1, 3, 2 * G, 64, generator=g).to(IO[io]).cuda()
+    win = [torch.randn(1, 8, 2, 64, generator=g).cuda() for _ in range(2)]
+    clean = _run_attn(c, q, win, [90], [6])
+    for bad in (torch.finfo(torch.float32).max, torch.finfo(torch.float32).min, 3.3961775e38):
+        dirty = [win[0], win[1].clone()]
+        dirty[1][0, 89 % 8, 1, 5] = bad                   # the last position, head 1
+        out = _run_attn(c, q, dirty, [90], [6])
+        # a tile of exact tokens is summed another way then
+        assert (out[:, :2] - clean[:, :2]).abs().max() <= (2.0 ** -7 if io == "bf16" else 2.0 ** -19) * clean.abs().max()
+        assert torch.equal(out[:, 2, :G], clean[:, 2, :G])
+        kk, vv = (np.concatenate([x, kv8.ring_rows(_f64(r[0]), 90, 6)[:, 1]])
+                  for x, r in zip((c.values["k"][0][1], c.values["v"][0][1]), dirty))
+        for i in range(G):
+            ref, a = kv8.attend(_f64(q[0, 2, G + i]), kk, vv)
+            got = _f64(out[0, 2, G + i])
+            assert abs(got[5] - ref[5]) <= (2.0 ** -7 if io == "bf16" else 2.0 ** -17) * abs(ref[5])
+            assert np.all(np.abs(np.delete(got - ref, 5)) <= (2.0 ** -7 if io == "bf16" else 2.0 ** -17) * np.abs(vv[:, 6:]).max())
