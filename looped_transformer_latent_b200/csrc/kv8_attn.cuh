@@ -31,10 +31,13 @@
 #pragma once
 
 #include "kernels.cuh"
+#include "kv8_math.cuh"
 #include "tc_ptx.cuh"
 
 namespace lla {
 namespace kv8 {
+
+using ptx::ex2;                  // below 2^-126 it is 0
 
 constexpr int AT = 128;          // threads
 constexpr int AW = AT / 32;
@@ -44,18 +47,6 @@ __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
   asm("prmt.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(sel));
   return r;
 }
-__device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
-// two e4m3 codes in the low half of w -> f16x2
-__device__ __forceinline__ uint32_t e4m3_f16x2(uint32_t w) {
-  uint32_t r;
-  asm("{.reg .b16 l, h; mov.b32 {l, h}, %1; cvt.rn.f16x2.e4m3x2 %0, l;}" : "=r"(r) : "r"(w));
-  return r;
-}
-
 // Widening of codes to f16, exact.  lo, hi: the two lower and the two upper
 // bytes of a word; pairs: byte i of a beside byte i of b, for i = 0, 1 and 2, 3.
 // int8: the byte plus 128 in the low mantissa bits of 1024, less 1152 (1.25
@@ -95,11 +86,6 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], 
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
 __device__ __forceinline__ float2 unpack_f16(uint32_t h) {
   float2 r;
   asm("{.reg .f16 l, h; mov.b32 {l, h}, %2; cvt.f32.f16 %0, l; cvt.f32.f16 %1, h;}" : "=f"(r.x), "=f"(r.y) : "r"(h));
@@ -123,14 +109,6 @@ __device__ __forceinline__ void split_bf16(float x, float y, uint32_t (&o)[T]) {
     x -= u.x; y -= u.y;
   }
 }
-// 2^x; below 2^-126 it is 0
-__device__ __forceinline__ float ex2(float x) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
-// 2^e, -126 <= e <= 127
-__device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }
 // 8 x 8 transpose across the warp: lane (g, t) of (row g, columns 2t, 2t + 1)
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   uint32_t r;

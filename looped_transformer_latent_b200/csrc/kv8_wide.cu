@@ -28,12 +28,14 @@
 #include <type_traits>
 
 #include "kernels.cuh"
+#include "kv8_math.cuh"
 #include "tc_ptx.cuh"
 
 namespace lla {
 namespace {
 
 using namespace ptx;
+using namespace kv8;
 
 constexpr int TOK = 128;                       // tokens of a tile
 constexpr int CHUNK = TOK * 128;               // bytes of 128 rows of 64 f16 elements
@@ -71,21 +73,6 @@ __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatil
   }
 }
 
-__device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
-__device__ __forceinline__ uint32_t e4m3_f16x2(uint32_t w) {
-  uint32_t r;
-  asm("{.reg .b16 l, h; mov.b32 {l, h}, %1; cvt.rn.f16x2.e4m3x2 %0, l;}" : "=r"(r) : "r"(w));
-  return r;
-}
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
 // Two elements at a time, each rounded by itself (never one operation with the next).
 __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
   float2 r;
@@ -99,8 +86,6 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
       : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
   return r;
 }
-__device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }
-
 // 4 codes to f16, in order (int8: the byte plus 128 in the low bits of 1024, less 1152)
 template <int CODE>
 __device__ __forceinline__ uint2 widen4(uint32_t w) {
