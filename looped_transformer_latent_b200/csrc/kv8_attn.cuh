@@ -25,7 +25,7 @@
 // pipe); 16 x 55 heads of 96, 32 rows, 4096 int8 tokens take 235 us (3.0 TB/s).
 // fp32 queries double the products and add their sums apart: 585 instructions for
 // 16 tokens of one tile of 8 rows, 2.2 a cycle from 15 warps an SM, 300 MB of
-// 96-element heads with their weights in 99 us.  Rings and not register prefetch:
+// 96-element heads with their weights in 103 us.  Rings and not register prefetch:
 // with 8 warps an SM the registers held 24 KB under way, half of what the memory's
 // latency asks for (462 us).
 #pragma once
@@ -197,9 +197,8 @@ constexpr int kQExp = 13;
 // times kLow, and meets the codes first; its products are taken back by that
 // power of two, and what is lost lies 39 bits below the largest (without it a flat
 // rest of 4096 tokens of a warp, 25 bits below a peak, was lost: 1e-4 of the output).
-// References are whole
-// numbers, so that moving one is exact, and of a only m - a is kept, which means
-// the same however large the logits are.
+// References are whole numbers, so that moving one is exact, and of a only m - a is
+// kept, which means the same however large the logits are.
 constexpr float kSlack = 12.f, kMost = 15.f, kUnset = -3.4e38f;
 constexpr float kLow = 0x1p12f, kLowInv = 0x1p-12f;
 // from here on the rounding of a product exceeds the slack of f16, and the difference to a reference is taken from
