@@ -441,10 +441,9 @@ _pack_attn = _packer(_abi.Kv8AttnParams, _CACHE_FMT + _I32_FMT + "2i2Pi4x4q2P2i3
 _pack_evict = _packer(_abi.Kv8EvictParams, 2 * _CACHE_FMT + "P2qP2q2P3i4xP")
 
 
-def _like(a, b):
-    """Whether a and b have one shape and one layout; an axis of one element may carry any stride."""
-    shape, sa, sb = a.shape, a.stride(), b.stride()
-    return shape == b.shape and (sa == sb or all(n <= 1 or x == y for n, x, y in zip(shape, sa, sb)))
+def _unlike(shape, sa, sb):
+    """Whether strides that are not equal make two layouts of shape: an axis of one element may carry any."""
+    return any(n > 1 and x != y for n, x, y in zip(shape, sa, sb))
 
 
 def _kv8_cache(k8, v8, k_scale, v_scale):
@@ -459,9 +458,9 @@ def _kv8_cache(k8, v8, k_scale, v_scale):
         raise TypeError(f"unsupported code dtype {dtype}; use int8 or float8_e4m3fn")
     if v8.dtype is not dtype or k_scale.dtype is not torch.float32 or v_scale.dtype is not torch.float32:
         raise TypeError("k8 and v8 share a dtype, scales are float32")
-    if len(shape) != 4 or not _like(k8, v8):
+    if len(shape) != 4 or v8.shape != shape or (v8.stride() != st and _unlike(shape, v8.stride(), st)):
         raise ValueError("k8 and v8 are [B,H,Ncap,d] with the same strides")
-    if len(sshape) != 3 or not _like(k_scale, v_scale):
+    if len(sshape) != 3 or v_scale.shape != sshape or (v_scale.stride() != ss and _unlike(sshape, v_scale.stride(), ss)):
         raise ValueError("k_scale and v_scale are [B,H,Ncap/block] with the same strides")
     B, H, cap, d = shape
     sB, sH, nb = sshape
@@ -569,7 +568,8 @@ def lla_kv8_write(*, k, v, k8, v8, k_scale, v_scale, n=None, max_n=None, src0=0,
     dev = _kv8_device(k, v, k8, v8, k_scale, v_scale, n, src0, row0)
     c = _kv8_cache(k8, v8, k_scale, v_scale)
     B, shape = c[0], k.shape
-    if len(shape) != 4 or not _like(k, v) or k.dtype is not v.dtype:
+    if (len(shape) != 4 or v.shape != shape or k.dtype is not v.dtype
+            or (k.stride() != v.stride() and _unlike(shape, k.stride(), v.stride()))):
         raise ValueError("k and v are [B,rows,H,d] and match in shape, strides and dtype")
     rows = shape[1]
     if shape[0] != B or shape[2] != c[1] or shape[3] != c[2]:
@@ -601,7 +601,8 @@ def _kv8_attn_params(q, k8, v8, k_scale, v_scale, lens, out, win_k=None, win_v=N
     win = (0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0)
     if win_k is not None:
         ws = win_k.shape
-        if win_v is None or len(ws) != 4 or not _like(win_k, win_v) or win_k.dtype is not win_v.dtype:
+        if (win_v is None or len(ws) != 4 or win_v.shape != ws or win_k.dtype is not win_v.dtype
+                or (win_k.stride() != win_v.stride() and _unlike(ws, win_k.stride(), win_v.stride()))):
             raise ValueError("win_k and win_v are [B,Wcap,H,d] and match in shape, strides and dtype")
         if ws[0] != B or ws[2] != H or ws[3] != d:
             raise ValueError("win_k and win_v are [B,Wcap,H,d] of the cache's B, H and d")
